@@ -34,6 +34,20 @@ class Layer(ctypes.Structure):
                 ("mode", ctypes.c_int32)]
 
 
+NORM_KINDS = {None: 0, "rms": 1, "layer": 2}
+
+
+class Norm(ctypes.Structure):
+    """struct lynx_norm (include/lynx.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in
+                 ("x", "y", "gate", "post_weight", "post_bias", "weight", "bias", "scale", "shift",
+                  "x_out", "h", "q", "q_scale")]
+                + [(n, ctypes.c_int64) for n in ("M", "C", "samples", "gate_stride",
+                                                 "scale_stride", "shift_stride")]
+                + [(n, ctypes.c_float) for n in ("residual_scale", "post_eps", "eps")]
+                + [(n, ctypes.c_int32) for n in ("x_fp32", "post_norm", "norm")])
+
+
 # every symbol the public headers declare, with (restype, argtypes)
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _LP = ctypes.POINTER(Layer)
@@ -49,6 +63,12 @@ SIGNATURES = {
     "lynx_linear_dense": (_I, [_P, _P, _P, _I64, _I64, _I64, _P]),
     "lynx_sequence_workspace_bytes": (_SZ, [_LP, _I64]),
     "lynx_linear_sequence": (_I, [_LP, _I64, _P, _SZ, _P]),
+    "lynx_quantize_fp8": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "lynx_quantize_fp8_weight": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "lynx_fp8_workspace_bytes": (_SZ, [_I64, _I64]),
+    "lynx_linear_fp8": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "lynx_linear_fp8_packed": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "lynx_block_norm": (_I, [ctypes.POINTER(Norm), _P]),
     "lynx_probe_mfma": (_I, [_I, _I, _P, _P, _P, _P, _P]),
     "lynx_probe_mfma_rate": (_I, [_I, _I, _I, _P, _P, _P]),
 }
@@ -277,6 +297,217 @@ def linear_sequence(layers: list, workspace=None):
                                       0 if workspace is None else workspace.numel(),
                                       _stream(dev)),
            "lynx_linear_sequence")
+
+
+# ---- 8-bit linear layer and block norms ---------------------------------------
+
+FP8, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _expect(t, dtype, shape, dev, name) -> int:
+    """The data pointer of a contiguous device tensor of this type and shape on
+    `dev`; raises as _need does."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+        _need(t, dtype, shape, name)
+        raise ValueError(f"{name}: expected a tensor on {dev}, got one on {t.device}")
+    return t.data_ptr()
+
+
+def _matrix(t, name):
+    """(rows, columns, device) of a 2-d device tensor."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got shape {tuple(t.shape)}")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: must be a device tensor")
+    return t.shape[0], t.shape[1], dev
+
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """Calls the entry point on `dev`'s current stream, with `dev` as the
+    current device (the library works on the current device)."""
+    f = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        _check(f(*args, _stream(dev)), fn)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream(dev)), fn)
+
+
+def _scale_words(K: int) -> int:
+    return (K + 511) // 512
+
+
+def quantize_fp8(X: torch.Tensor, out: tuple | None = None):
+    """The 8-bit operand of an activation (lynx_quantize_fp8).
+
+    Returns (q, scale): q [M, K] float8_e4m3fn and scale [ceil(K/512), M, 4]
+    float8_e8m0fnu, the scale of row m and channels 128 kb .. 128 kb + 127 at
+    scale[kb // 4, m, kb % 4].  out: the pair of tensors to write.
+    """
+    M, K, dev = _matrix(X, "X")
+    x = _expect(X, torch.bfloat16, (M, K), dev, "X")
+    shape = (_scale_words(K), M, 4)
+    q, scale = out if out is not None else (torch.empty((M, K), dtype=FP8, device=dev),
+                                            torch.empty(shape, dtype=E8M0, device=dev))
+    _call("lynx_quantize_fp8", dev, x, M, K, _expect(q, FP8, (M, K), dev, "q"),
+          _expect(scale, E8M0, shape, dev, "scale"))
+    return q, scale
+
+
+def quantize_fp8_weight(W: torch.Tensor, out: tuple | None = None):
+    """The 8-bit operand of a weight (lynx_quantize_fp8_weight).
+
+    Returns (q, scale): q [N, K] float8_e4m3fn and scale [ceil(N/128),
+    4 ceil(K/512)] float8_e8m0fnu, the scale of the block of 128 rows x 128
+    channels (nb, kb) at scale[nb, kb].  out: the pair of tensors to write.
+    """
+    N, K, dev = _matrix(W, "W")
+    w = _expect(W, torch.bfloat16, (N, K), dev, "W")
+    shape = ((N + 127) // 128, 4 * _scale_words(K))
+    q, scale = out if out is not None else (torch.empty((N, K), dtype=FP8, device=dev),
+                                            torch.empty(shape, dtype=E8M0, device=dev))
+    _call("lynx_quantize_fp8_weight", dev, w, N, K, _expect(q, FP8, (N, K), dev, "q"),
+          _expect(scale, E8M0, shape, dev, "scale"))
+    return q, scale
+
+
+def fp8_workspace_bytes(M: int, K: int) -> int:
+    return lib().lynx_fp8_workspace_bytes(M, K)
+
+
+def _fp8_weight(Wq, Ws, K, dev):
+    N = Wq.shape[0]
+    return (N, _expect(Wq, FP8, (N, K), dev, "Wq"),
+            _expect(Ws, E8M0, ((N + 127) // 128, 4 * _scale_words(K)), dev, "Ws"))
+
+
+def linear_fp8(X, Wq, Ws, Y=None, workspace=None):
+    """Y = Q(X) W^T with the weight (Wq, Ws) of quantize_fp8_weight (lynx_linear_fp8)."""
+    M, K, dev = _matrix(X, "X")
+    x = _expect(X, torch.bfloat16, (M, K), dev, "X")
+    N, wq, ws = _fp8_weight(Wq, Ws, K, dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    y = _expect(Y, torch.bfloat16, (M, N), dev, "Y")
+    if workspace is None:
+        workspace = torch.empty((max(fp8_workspace_bytes(M, K), 1),), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be a contiguous tensor on {dev}")
+    _call("lynx_linear_fp8", dev, x, wq, ws, y, M, N, K, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return Y
+
+
+def linear_fp8_packed(q, scale, Wq, Ws, Y=None):
+    """Y = X W^T of two 8-bit operands, (q, scale) of quantize_fp8 or a block norm
+    and (Wq, Ws) of quantize_fp8_weight (lynx_linear_fp8_packed)."""
+    M, K, dev = _matrix(q, "q")
+    xq = _expect(q, FP8, (M, K), dev, "q")
+    xs = _expect(scale, E8M0, (_scale_words(K), M, 4), dev, "scale")
+    N, wq, ws = _fp8_weight(Wq, Ws, K, dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _call("lynx_linear_fp8_packed", dev, xq, xs, wq, ws,
+          _expect(Y, torch.bfloat16, (M, N), dev, "Y"), M, N, K)
+    return Y
+
+
+def _sample_rows(t, C, dev, name):
+    """(pointer, rows, stride) of per-sample parameters [rows, C] (or [C]); the
+    rows may lie apart, as in a slice of a modulation projection's output."""
+    if t is None:
+        return None, 1, 0
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dim() not in (1, 2) or t.shape[-1] != C:
+        raise ValueError(f"{name}: expected shape (samples, {C}) or ({C},), got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got one on {t.device}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: its channels must be contiguous")
+    if t.dim() == 1 or t.shape[0] == 1:
+        return t.data_ptr(), 1, 0
+    return t.data_ptr(), t.shape[0], t.stride(0)
+
+
+def _block_norm(x, y, gate, post_norm, post_weight, post_bias, post_eps, residual_scale, norm,
+                weight, bias, scale, shift, eps, fp8, x_out, out):
+    M, C, dev = _matrix(x, "x")
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+        raise TypeError(f"x: expected torch.bfloat16 or torch.float32, got {x.dtype}")
+    if norm not in NORM_KINDS or post_norm not in NORM_KINDS:
+        raise ValueError(f"a norm is one of {list(NORM_KINDS)}")
+    a = Norm(x=_expect(x, x.dtype, (M, C), dev, "x"), M=M, C=C, samples=1,
+             residual_scale=residual_scale, post_eps=post_eps, eps=eps,
+             x_fp32=x.dtype is torch.float32, post_norm=NORM_KINDS[post_norm],
+             norm=NORM_KINDS[norm])
+    if y is not None:
+        a.y = _expect(y, torch.bfloat16, (M, C), dev, "y")
+        if x_out is None:
+            x_out = torch.empty_like(x)
+        a.x_out = _expect(x_out, x.dtype, (M, C), dev, "x_out")
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("weight", weight),
+                    ("bias", bias)):
+        if t is not None:
+            setattr(a, name, _expect(t, torch.bfloat16, (C,), dev, name))
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is not None:
+            p, rows, stride = _sample_rows(t, C, dev, name)
+            setattr(a, name, p)
+            setattr(a, name + "_stride", stride)
+            if rows != 1:
+                if a.samples not in (1, rows):
+                    raise ValueError(f"{name}: {rows} samples, and {a.samples} elsewhere")
+                a.samples = rows
+    if norm is None:
+        if fp8 or out is not None:
+            raise ValueError("without a norm there is no second output")
+    elif fp8:
+        shape = (_scale_words(C), M, 4)
+        if out is None:
+            out = (torch.empty((M, C), dtype=FP8, device=dev),
+                   torch.empty(shape, dtype=E8M0, device=dev))
+        a.q = _expect(out[0], FP8, (M, C), dev, "q")
+        a.q_scale = _expect(out[1], E8M0, shape, dev, "q_scale")
+    else:
+        if out is None:
+            out = torch.empty((M, C), dtype=torch.bfloat16, device=dev)
+        a.h = _expect(out, torch.bfloat16, (M, C), dev, "h")
+    _call("lynx_block_norm", dev, ctypes.byref(a))
+    return x_out, out
+
+
+def norm_modulate(x, norm="rms", weight=None, bias=None, scale=None, shift=None, eps=1e-6,
+                  fp8=False, out=None):
+    """h = norm(x) * (1 + scale[b]) + shift[b], the norm before a block (lynx_block_norm).
+
+    x [M, C] bf16 or fp32; norm "rms" or "layer", with optional weight and bias
+    [C]; scale, shift [samples, C] (or [C]), samples of M / samples rows each,
+    their rows any multiple of 8 elements apart.  Returns h [M, C] bf16, or with
+    fp8=True the 8-bit operand (q, scale) as quantize_fp8 lays it out.
+    out: the tensor (or pair) to write.
+    """
+    if norm is None:
+        raise ValueError("norm_modulate needs a norm")
+    return _block_norm(x, None, None, None, None, None, 0.0, 1.0, norm, weight, bias, scale, shift,
+                       eps, fp8, None, out)[1]
+
+
+def residual_norm(x, y, gate=None, post_norm=None, post_weight=None, post_bias=None,
+                  post_eps=1e-6, residual_scale=1.0, norm=None, weight=None, bias=None, scale=None,
+                  shift=None, eps=1e-6, fp8=False, x_out=None, out=None):
+    """x' = residual_scale * x + gate[b] * post_norm(y), and the next block's
+    h = norm(x') * (1 + scale[b]) + shift[b], in one pass (lynx_block_norm).
+
+    x [M, C] bf16 or fp32 and y [M, C] bf16; the other arguments as in
+    norm_modulate, gate [samples, C] (or [C]).  Returns (x', h): x' in x's type
+    (x_out may be x), h as norm_modulate returns it, None with norm=None.
+    """
+    if y is None:
+        raise ValueError("residual_norm needs y; use norm_modulate without a branch")
+    return _block_norm(x, y, gate, post_norm, post_weight, post_bias, post_eps, residual_scale,
+                       norm, weight, bias, scale, shift, eps, fp8, x_out, out)
 
 
 # dense-equivalent flops of one instruction of each probe kind: smfmac

@@ -23,10 +23,7 @@ constexpr int64_t kMaxElems = int64_t(1) << 31;
 // the dimensions padded by one tile the tensors stay below 2^31 elements, so
 // those offsets stay below 2^32 and never wrap into the tensor.
 constexpr int64_t kPad = 256;
-
-inline size_t round_up256(size_t x) { return (x + 255) & ~size_t(255); }
-
-bool rank_ok(int64_t R) { return R == 0 || R == 16 || R == 32 || R == 48 || R == 64; }
+}  // namespace
 
 bool dims_ok(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K <= 0) return false;
@@ -36,6 +33,9 @@ bool dims_ok(int64_t M, int64_t N, int64_t K) {
         return false;
     return true;
 }
+
+namespace {
+bool rank_ok(int64_t R) { return R == 0 || R == 16 || R == 32 || R == 48 || R == 64; }
 
 struct WorkspaceLayout {
     size_t values, meta, scale, T, total;

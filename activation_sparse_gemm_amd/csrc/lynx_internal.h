@@ -28,6 +28,11 @@ inline lynx_status launch_status() {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline size_t round_up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// The shape limits of lynx.h for X [M][K], W [N][K], Y [M][N].
+bool dims_ok(int64_t M, int64_t N, int64_t K);
+
 // ---- the sparse layer, shared by the entry points -------------------------
 // Argument checks of the sparse + LoRA layer (everything but its workspace);
 // LYNX_OK with *noop set when M or N is 0.

@@ -1,5 +1,6 @@
 /*
- * lynx.h - C ABI of the RT-Lynx sparse + LoRA linear layer for AMD MI355X (gfx950).
+ * lynx.h - C ABI of the RT-Lynx sparse + LoRA linear layer for AMD MI355X (gfx950),
+ * its dense and 8-bit alternatives, and the norms that stand between such layers.
  *
  * The layer (RT-Lynx page, aitrends.kr, "RT-Lynx: Diffusion Transformers에서
  * GEMM Sparsity를 Activation으로 옮겨 실현하는 방법"; section 방법론, item
@@ -224,6 +225,122 @@ size_t lynx_sequence_workspace_bytes(const lynx_layer* layers, int64_t n);
  */
 lynx_status lynx_linear_sequence(const lynx_layer* layers, int64_t n, void* workspace,
                                  size_t workspace_bytes, lynx_stream_t stream);
+
+/*
+ * ---- 8-bit linear layer -----------------------------------------------------
+ * Y = Q(X) Q(W)^T with both operands in e4m3 (OCP: 4 exponent bits, 3 fraction
+ * bits, largest value 448) and one power-of-two scale per block of 128:
+ *   - an activation has a scale for every 128 consecutive channels of a row, a
+ *     weight one for every block of 128 rows x 128 channels, both aligned at 0
+ *     (where K % 128 == 64 the last block has 64 channels);
+ *   - a block whose largest magnitude is a gets the scale 2^e with the smallest
+ *     integer e >= -127 that keeps a <= 448 * 2^e (a = 0: e = 0), and the values
+ *     x * 2^-e rounded to nearest even.  x * 2^-e is exact, so values and scales
+ *     are those of the definition, bit for bit;
+ *   - the scale is stored as its E8M0 byte e + 127.  A block that holds a NaN or
+ *     an infinity gets the byte 255 (NaN) and unspecified values, and every
+ *     output made from it is NaN.  (This path defines them; the rest of the
+ *     library leaves non-finite inputs unspecified.)
+ * The product takes any operand of this form, also one quantised elsewhere:
+ *   Y[m][n] = sum over K blocks kb of 2^(eX[m][kb] + eW[n/128][kb]) *
+ *             sum over k in kb of Xq[m][k] Wq[n][k],
+ * one rounding to bf16.  The matrix instruction adds products in groups of 8
+ * channels, keeping bits down to 2^-13 of the group's largest product, and adds the
+ * groups and the accumulator in fp32.
+ *
+ * Storage: values row-major, Xq [M][K] and Wq [N][K] bytes.
+ *   Activation scales [KW][M][4] bytes, KW = ceil(K / 512): the byte of row m and
+ *     block kb at ((kb / 4) * M + m) * 4 + kb % 4 (four blocks of a row to a word).
+ *   Weight scales [ceil(N / 128)][4 * KW] bytes: block (nb, kb) at nb * 4 * KW + kb.
+ *   Places of blocks past K are written as 127 and never used.
+ * Shape limits and conventions as above (K a positive multiple of 64).
+ */
+
+/* X [M][K] bf16 -> q [M][K], scale [KW][M][4]. */
+lynx_status lynx_quantize_fp8(const uint16_t* X, int64_t M, int64_t K, uint8_t* q,
+                              uint8_t* scale, lynx_stream_t stream);
+
+/* W [N][K] bf16 -> q [N][K], scale [ceil(N/128)][4 KW]. */
+lynx_status lynx_quantize_fp8_weight(const uint16_t* W, int64_t N, int64_t K, uint8_t* q,
+                                     uint8_t* scale, lynx_stream_t stream);
+
+/*
+ * Bytes of device workspace lynx_linear_fp8 needs for an (M, K) activation: its
+ * values and scales, each 256-byte aligned.  Returns 0 for invalid sizes.
+ */
+size_t lynx_fp8_workspace_bytes(int64_t M, int64_t K);
+
+/*
+ * The whole layer: quantises X into `workspace`, then the product.
+ * Inputs: X [M][K] bf16; Wq, Ws a quantised weight [N][K].  Output: Y [M][N] bf16.
+ * workspace: >= lynx_fp8_workspace_bytes(M, K) bytes, 256-byte aligned, contents
+ * on entry irrelevant, clobbered.
+ */
+lynx_status lynx_linear_fp8(const uint16_t* X, const uint8_t* Wq, const uint8_t* Ws, uint16_t* Y,
+                            int64_t M, int64_t N, int64_t K, void* workspace,
+                            size_t workspace_bytes, lynx_stream_t stream);
+
+/* The product alone, on a quantised activation Xq, Xs. */
+lynx_status lynx_linear_fp8_packed(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
+                                   const uint8_t* Ws, uint16_t* Y, int64_t M, int64_t N,
+                                   int64_t K, lynx_stream_t stream);
+
+/*
+ * ---- block norms ------------------------------------------------------------
+ * What stands between two linear layers of a transformer block, in one pass:
+ *   z  = post(y)                            the norm after the branch
+ *   x' = residual_scale * x + gate[b] * z   the residual stream, stored in x_out
+ *   h  = pre(x') * (1 + scale[b]) + shift[b]   the next branch's input
+ * post and pre are each one of
+ *   LYNX_NORM_NONE    post: z = y.  pre: no h (h, q and pre's parameters NULL);
+ *   LYNX_NORM_RMS     v / sqrt(mean(v^2) + eps) * weight + bias;
+ *   LYNX_NORM_LAYER   (v - mean(v)) / sqrt(var(v) + eps) * weight + bias;
+ * over the C channels of a row, with an absent (NULL) weight, scale or gate read
+ * as no factor and an absent bias or shift as no term.  Rows are samples of
+ * M / samples rows each, b the row's sample.  All arithmetic is fp32, and h is
+ * taken from x' before x' is rounded for x_out.
+ *   - y == NULL: no branch; x' = x, and x_out, gate, post_weight and post_bias are
+ *     NULL and residual_scale is not used.
+ *   - h is written as bf16 to `h`, or as the 8-bit operand (quantised from the
+ *     fp32 h; C % 64 == 0) to `q` [M][C] and `q_scale`: exactly one form is given
+ *     when pre is not LYNX_NORM_NONE.
+ *   - x and x_out are bf16, or fp32 where x_fp32 is not 0.  x_out may be x; no
+ *     other output may overlap an input.
+ *   - A non-finite value makes its own row's outputs NaN or infinite as fp32
+ *     arithmetic does, and no other row's.
+ * Limits: C a multiple of 8, 8 <= C <= 16384; 0 <= M <= 2^23 (0 is a no-op);
+ * samples >= 1 divides M; strides (in elements, from one sample's row to the
+ * next; 0 = one row for all) >= 0 and multiples of 8; eps and post_eps >= 0.
+ * Every pointer is 16-byte aligned.
+ */
+typedef enum lynx_norm_kind {
+    LYNX_NORM_NONE = 0,
+    LYNX_NORM_RMS = 1,
+    LYNX_NORM_LAYER = 2
+} lynx_norm_kind;
+
+typedef struct lynx_norm {
+    const void* x;                /* [M][C] bf16 or fp32 */
+    const uint16_t* y;            /* [M][C] bf16, or NULL */
+    const uint16_t* gate;         /* samples rows of C bf16, gate_stride apart, or NULL */
+    const uint16_t* post_weight;  /* [C] bf16 or NULL; NULL if post_norm is NONE */
+    const uint16_t* post_bias;    /* [C] bf16 or NULL; NULL if post_norm is NONE */
+    const uint16_t* weight;       /* [C] bf16 or NULL */
+    const uint16_t* bias;         /* [C] bf16 or NULL */
+    const uint16_t* scale;        /* samples rows, scale_stride apart, or NULL */
+    const uint16_t* shift;        /* samples rows, shift_stride apart, or NULL */
+    void* x_out;                  /* [M][C] as x; NULL iff y is NULL */
+    uint16_t* h;                  /* [M][C] bf16, or NULL */
+    uint8_t* q;                   /* [M][C] e4m3, or NULL */
+    uint8_t* q_scale;             /* [ceil(C/512)][M][4], NULL iff q is NULL */
+    int64_t M, C, samples;
+    int64_t gate_stride, scale_stride, shift_stride;
+    float residual_scale, post_eps, eps;
+    int32_t x_fp32;
+    int32_t post_norm, norm;      /* lynx_norm_kind */
+} lynx_norm;
+
+lynx_status lynx_block_norm(const lynx_norm* norm, lynx_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,333 @@
+"""The 8-bit linear layer and its quantisers against the fp64 oracle.
+
+Values and scales are compared bit for bit (x * 2^-e is exact, so the definition
+leaves one answer).  Tolerance of the product, per element: half a bf16 step,
+2^-8 |y|, plus the sums.  The matrix instruction adds products in groups of 8,
+keeping bits down to 2^-13 of the group's largest product
+(test_instruction_keeps_13_bits_below_a_groups_largest_product): each of the other 7
+loses less than 2^-13 of it, at most 7 2^-13 sum |x w| in all.  The groups' sums and
+the accumulator are added in fp32: (K / 64 + 64) 2^-23 sum |x w| for K / 64
+instructions and the joins, each rounding by at most 2^-23 (nearest or truncated) of a
+partial sum that sum |x w| bounds.  Errors of that size do not add up in practice,
+so every row also meets the library's bar of 5e-3 relative error.
+"""
+import numpy as np
+import pytest
+import torch
+
+import activation_sparse_gemm_amd as lynx
+import tests.gpu_util as gu
+from oracle import block_oracle as bo
+from oracle.lynx_oracle import decode_bf16
+from tests.gpu_util import dev, host_bits, host_f64, say
+from workloads import bf16_bits_from_f32, make_activation
+
+pytestmark = pytest.mark.gpu
+
+FP8, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def u8(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy()
+
+
+def fp8_dev(codes):
+    return torch.from_numpy(np.ascontiguousarray(codes)).cuda().view(FP8)
+
+
+def e8_dev(b):
+    return torch.from_numpy(np.ascontiguousarray(b)).cuda().view(E8M0)
+
+
+def poison(shape, dtype):
+    return torch.full(shape, 0xFF, dtype=torch.uint8, device="cuda").view(dtype)
+
+
+def heavy(M, K, seed):
+    """Activation bits and their values (heavy tails, outlier channels, post-GELU for odd seeds)."""
+    b = make_activation("gelu" if seed % 2 else "heavy", M, K, seed)
+    return b, decode_bf16(b)
+
+
+def operand(M, K, seed):
+    """A quantised activation as the oracle makes it: device tensors and values."""
+    _, x = heavy(M, K, seed)
+    codes, byte = bo.quantize(x)
+    return fp8_dev(codes), e8_dev(bo.stored_scales(byte)), bo.values(codes, byte)
+
+
+def weight(N, K, seed):
+    w = np.random.default_rng(seed).standard_normal((N, K)) * K ** -0.5
+    # blocks of unlike sizes, so that a wrong block's scale shows
+    w *= np.exp2(np.random.default_rng(seed + 1).integers(-3, 4, (-(-N // 128), -(-K // 128))).astype(float)
+                 ).repeat(128, 0)[:N].repeat(128, 1)[:, :K]
+    codes, byte = bo.quantize_weight(w)
+    return fp8_dev(codes), e8_dev(bo.stored_weight_scales(byte)), bo.values(codes, byte, 128)
+
+
+def product_arith(K):
+    """The sums' error as a share of sum |x w| (see above)."""
+    return 7 * 2.0 ** -13 + (K / 64 + 64) * 2.0 ** -23
+
+
+def check_product(Y, xv, wv, label):
+    K = xv.shape[1]
+    ref, mag = bo.linear(xv, wv)
+    got = host_f64(Y)
+    tol = 2.0 ** -8 * np.abs(ref) + product_arith(K) * mag
+    off = np.abs(got - ref)
+    say(f"{label}: max error / tolerance {np.max(off / np.maximum(tol, 1e-300)):.3f}")
+    assert np.isfinite(got).all() and (off <= tol).all(), label
+    assert gu.row_rel_err(got, ref).max() <= gu.ROW_REL_TOL, label
+
+
+# ---- quantisers --------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,K", [(1, 64), (1, 128), (3, 192), (7, 512), (33, 576), (333, 1472),
+                                 (77, 3072), (5, 12288), (2101, 4160), (16391, 64)])
+def test_quantize_bits(M, K):
+    bits, x = heavy(M, K, M + K)
+    say(f"quantize_fp8 M={M} K={K}")
+    q, s = lynx.quantize_fp8(dev(bits), out=(poison((M, K), FP8), poison(((K + 511) // 512, M, 4), E8M0)))
+    torch.cuda.synchronize()
+    codes, byte = bo.quantize(x)
+    assert np.array_equal(u8(s), bo.stored_scales(byte))
+    assert np.array_equal(u8(q), codes)
+
+
+@pytest.mark.parametrize("N,K", [(1, 64), (16, 128), (128, 128), (130, 192), (257, 576), (1000, 832), (384, 3072)])
+def test_quantize_weight_bits(N, K):
+    w = np.random.default_rng(N).standard_normal((N, K)).astype(np.float32) * np.float32(K ** -0.5)
+    w *= np.exp2(np.arange(N) // 128 % 5 - 2.0)[:, None].astype(np.float32)
+    bits = bf16_bits_from_f32(w)
+    say(f"quantize_fp8_weight N={N} K={K}")
+    q, s = lynx.quantize_fp8_weight(dev(bits), out=(
+        poison((N, K), FP8), poison(((N + 127) // 128, (K + 511) // 512 * 4), E8M0)))
+    torch.cuda.synchronize()
+    codes, byte = bo.quantize_weight(decode_bf16(bits))
+    assert np.array_equal(u8(s), bo.stored_weight_scales(byte))
+    assert np.array_equal(u8(q), codes)
+
+
+def special_rows():
+    """Rows of 256 channels where the scale or the rounding can go wrong."""
+    rng = np.random.default_rng(7)
+    rows = [np.zeros(256), -np.zeros(256), np.full(256, 2.0 ** -133), np.full(256, -(2.0 ** 127) * (2 - 2.0 ** -7))]
+    for e in (-100, -9, 0, 1, 100):                   # at 448 2^e, one bf16 step above, one below
+        for a in (448.0, 450.0, 446.0):
+            r = rng.uniform(-1, 1, 256) * 400 * 2.0 ** e
+            r[17] = a * 2.0 ** e
+            rows.append(r)
+    r = np.full(256, 2.0 ** -20)                      # far below the block's largest: subnormal and zero codes
+    r[::2] = 448 * 2.0 ** -rng.integers(0, 30, 128)
+    rows.append(r)
+    return bf16_bits_from_f32(np.array(rows, dtype=np.float32))
+
+
+def test_quantize_special_values():
+    bits = special_rows()
+    say("quantize_fp8 special values")
+    q, s = lynx.quantize_fp8(dev(bits))
+    wq, ws = lynx.quantize_fp8_weight(dev(bits))
+    torch.cuda.synchronize()
+    x = decode_bf16(bits)
+    codes, byte = bo.quantize(x)
+    assert np.array_equal(u8(s), bo.stored_scales(byte))
+    same = (u8(q) == codes) | ((codes & 0x7F == 0) & (u8(q) & 0x7F == 0))  # -0 may stand for 0
+    assert same.all()
+    codes, byte = bo.quantize_weight(x)
+    assert np.array_equal(u8(ws), bo.stored_weight_scales(byte))
+    assert ((u8(wq) == codes) | ((codes & 0x7F == 0) & (u8(wq) & 0x7F == 0))).all()
+
+
+@pytest.mark.parametrize("M,N", [(20, 40), (1100, 1000)])
+def test_non_finite_values_reach_their_row_only(M, N):
+    K = 320
+    bits, _ = heavy(M, K, 3)
+    bits = bits.copy()
+    bits[2, 5] = 0x7FC0        # NaN in block 0
+    bits[7, 300] = 0xFF80      # -inf in the half-filled block 2
+    bits[11, 130] = 0x7F80
+    say(f"quantize_fp8 + product with NaN and Inf M={M} N={N}")
+    q, s = lynx.quantize_fp8(dev(bits))
+    wq, ws, _ = weight(N, K, 5)
+    Y = host_f64(lynx.linear_fp8_packed(q, s, wq, ws))
+    sb = u8(s)
+    assert sb[0, 2, 0] == 255 and sb[0, 7, 2] == 255 and sb[0, 11, 1] == 255
+    assert (sb == 255).sum() == 3
+    bad = np.zeros(M, dtype=bool)
+    bad[[2, 7, 11]] = True
+    assert np.isnan(Y[bad]).all() and np.isfinite(Y[~bad]).all()
+    # and a weight block's NaN scale reaches the block's columns only
+    wb = u8(ws).copy()
+    wb[0, 1] = 255
+    q, s, _ = operand(M, K, 4)
+    Y = host_f64(lynx.linear_fp8_packed(q, s, wq, e8_dev(wb)))
+    assert np.isnan(Y[:, :128]).all() and np.isfinite(Y[:, 128:]).all()
+
+
+# ---- the product -------------------------------------------------------------------
+
+SHAPES = [(1, 64, 1), (1, 128, 32), (2, 3072, 640), (16, 192, 17), (17, 320, 33), (31, 576, 130),
+          (32, 12288, 64), (33, 64, 65), (64, 448, 200), (65, 1024, 127), (77, 3072, 384), (100, 640, 130),
+          (255, 960, 257), (300, 1152, 1000), (1000, 1472, 1102), (4096, 256, 64), (64, 256, 4100),
+          (1024, 64, 1024), (1030, 128, 1100), (1500, 704, 1288), (2048, 192, 1536), (700, 2112, 3000)]
+
+
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_product_shapes(M, K, N):
+    q, s, xv = operand(M, K, M + N)
+    wq, ws, wv = weight(N, K, N)
+    say(f"linear_fp8_packed M={M} K={K} N={N}")
+    Y = lynx.linear_fp8_packed(q, s, wq, ws, Y=gu.nan_bf16((M, N)))
+    torch.cuda.synchronize()
+    check_product(Y, xv, wv, f"product {M}x{K}->{N}")
+
+
+@pytest.mark.parametrize("M,K,N", [(4046, 640, 9100), (9216, 256, 3072), (4096, 3072, 12288)])
+def test_product_large_sampled_rows(M, K, N):
+    q, s, xv = operand(M, K, 2)
+    wq, ws, wv = weight(N, K, 9)
+    say(f"linear_fp8_packed M={M} K={K} N={N} sampled")
+    Y = lynx.linear_fp8_packed(q, s, wq, ws, Y=gu.nan_bf16((M, N)))
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(Y).all())
+    rows = np.unique(np.concatenate([gu.sample_rows(M, n=24, seed=1), np.arange(M - 30, M)]))
+    check_product(Y[torch.from_numpy(rows).cuda()], xv[rows], wv, f"product {M}x{K}->{N}")
+
+
+@pytest.mark.parametrize("M,K,N", [(8, 512, 40), (200, 384, 300), (1100, 640, 1030)])
+def test_product_exact_on_small_integers(M, K, N):
+    """Integers in -8..8, unlike powers of two per block: every partial sum is exact in fp32 and
+    the result checks lane, channel and scale assignment bit for bit."""
+    rng = np.random.default_rng(M)
+    xi, wi = rng.integers(-8, 9, (M, K)), rng.integers(-8, 9, (N, K))
+    kb = -(-K // 128)
+    xb = rng.integers(125, 130, (M, kb)).astype(np.uint8)
+    wb = rng.integers(125, 130, (-(-N // 128), kb)).astype(np.uint8)
+    xc, wc = bo.e4m3_encode(xi.astype(float)), bo.e4m3_encode(wi.astype(float))
+    say(f"exact product M={M} K={K} N={N}")
+    Y = lynx.linear_fp8_packed(fp8_dev(xc), e8_dev(bo.stored_scales(xb)), fp8_dev(wc),
+                               e8_dev(bo.stored_weight_scales(wb)), Y=gu.nan_bf16((M, N)))
+    ref = bo.values(xc, xb) @ bo.values(wc, wb, 128).T
+    assert np.array_equal(host_bits(Y), bf16_bits_from_f32(ref.astype(np.float32)))
+
+
+def test_instruction_keeps_13_bits_below_a_groups_largest_product():
+    """1 - 1 + 2^-13 in one group of 8 channels is exact; and products of unlike groups, and the
+    accumulator, are added in fp32: 2^-18 next to 1 and 2^-22 before 1 - 1 survive."""
+    def dot(K, items, scales=()):
+        x, w = np.zeros((32, K)), np.ones((32, K))
+        xb = np.full((32, -(-K // 128)), 127, dtype=np.uint8)
+        for k, v in items.items():
+            e = int(np.log2(abs(v)))
+            x[:, k], w[:, k] = np.sign(v) * 2.0 ** (e // 2), 2.0 ** (e - e // 2)
+        for b, e in scales:
+            xb[:, b] += np.uint8(e % 256)
+        Y = lynx.linear_fp8_packed(fp8_dev(bo.e4m3_encode(x)), e8_dev(bo.stored_scales(xb)),
+                                   fp8_dev(bo.e4m3_encode(w)),
+                                   e8_dev(bo.stored_weight_scales(np.full((1, xb.shape[1]), 127, np.uint8))))
+        return host_f64(Y)
+    say("instruction sums")
+    assert np.all(dot(128, {0: 1, 1: -1, 5: 2.0 ** -13}) == 2.0 ** -13)
+    assert np.all(dot(128, {0: 1, 1: -1, 20: 2.0 ** -18}) == 2.0 ** -18)
+    assert np.all(dot(128 * 17, {0: 1, 1024: 1, 2048: -1}, [(0, -22)]) == 2.0 ** -22)
+
+
+def test_product_extreme_scales():
+    """Scales at both ends whose product is an ordinary number, and one that is not."""
+    M, K, N = 40, 256, 136
+    ones = bo.e4m3_encode(np.ones((M, K)))
+    wc = bo.e4m3_encode(np.ones((N, K)))
+    for sx, sw, want in ((0, 254, 256.0), (254, 0, 256.0), (127, 127, 256.0), (20, 200, 256 * 2.0 ** -34)):
+        xb = np.full((M, 2), sx, dtype=np.uint8)
+        wb = np.full((2, 2), sw, dtype=np.uint8)
+        say(f"extreme scales {sx} {sw}")
+        Y = lynx.linear_fp8_packed(fp8_dev(ones), e8_dev(bo.stored_scales(xb)), fp8_dev(wc),
+                                   e8_dev(bo.stored_weight_scales(wb)))
+        assert np.all(host_f64(Y) == want), (sx, sw)
+
+
+# ---- the whole layer ---------------------------------------------------------------
+
+@pytest.mark.parametrize("M,K,N", [(1, 64, 40), (2, 3072, 1000), (15, 576, 130), (40, 1472, 70), (300, 640, 520),
+                                   (1300, 448, 1100)])
+def test_layer_is_quantiser_then_product(M, K, N):
+    bits, x = heavy(M, K, M)
+    wq, ws, wv = weight(N, K, 3)
+    X = dev(bits)
+    say(f"linear_fp8 M={M} K={K} N={N}")
+    Y = lynx.linear_fp8(X, wq, ws, Y=gu.nan_bf16((M, N)),
+                        workspace=gu.poisoned_bytes(lynx.fp8_workspace_bytes(M, K)))
+    check_product(Y, bo.values(*bo.quantize(x)), wv, f"layer {M}x{K}->{N}")
+    Y2 = lynx.linear_fp8_packed(*lynx.quantize_fp8(X), wq, ws)
+    assert torch.equal(Y.view(torch.int16), Y2.view(torch.int16))
+
+
+def test_empty_sizes():
+    wq, ws, _ = weight(40, 64, 1)
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
+    say("fp8 empty sizes")
+    q, s = lynx.quantize_fp8(x)
+    assert q.shape == (0, 64) and s.shape == (1, 0, 4)
+    assert lynx.linear_fp8(x, wq, ws).shape == (0, 40)
+    assert lynx.linear_fp8_packed(q, s, wq, ws).shape == (0, 40)
+    q, s = lynx.quantize_fp8_weight(x)
+    assert lynx.linear_fp8(torch.zeros((3, 64), dtype=torch.bfloat16, device="cuda"), q, s).shape == (3, 0)
+
+
+def test_python_checks_name_the_argument():
+    bits, _ = heavy(8, 128, 1)
+    X = dev(bits)
+    wq, ws, _ = weight(24, 128, 1)
+    q, s = lynx.quantize_fp8(X)
+    for call, err, name in [
+        (lambda: lynx.quantize_fp8(X.float()), TypeError, "X"),
+        (lambda: lynx.quantize_fp8(dev(heavy(8, 256, 1)[0])[:, ::2]), ValueError, "X"),
+        (lambda: lynx.linear_fp8(X, wq.view(torch.uint8), ws), TypeError, "Wq"),
+        (lambda: lynx.linear_fp8(X, wq, ws[:, :1]), ValueError, "Ws"),
+        (lambda: lynx.linear_fp8_packed(q, s.view(torch.uint8), wq, ws), TypeError, "scale"),
+        (lambda: lynx.linear_fp8_packed(q[:4], s, wq, ws), ValueError, "scale"),
+        (lambda: lynx.linear_fp8_packed(q, s, wq, ws.cpu()), ValueError, "Ws"),
+        (lambda: lynx.linear_fp8_packed(q, s, wq, ws, Y=torch.empty(8, 25, device="cuda", dtype=torch.bfloat16)),
+         ValueError, "Y"),
+    ]:
+        with pytest.raises(err, match=name):
+            call()
+    with pytest.raises(lynx.LynxError, match="LYNX_ERR_WORKSPACE"):
+        lynx.linear_fp8(X, wq, ws, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(lynx.LynxError, match="LYNX_ERR_SHAPE"):
+        lynx.quantize_fp8(torch.zeros((2, 96), dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("M,K,N", [(2, 512, 300), (60, 640, 256), (1100, 512, 1030)])
+def test_repeated_calls_two_streams_and_graph_replays_agree(M, K, N):
+    bits, _ = heavy(M, K, 8)
+    X = dev(bits)
+    wq, ws, _ = weight(N, K, 2)
+    say(f"fp8 repeat M={M} K={K} N={N}")
+    ref = lynx.linear_fp8(X, wq, ws).view(torch.int16).clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for st in streams:
+        with torch.cuda.stream(st):
+            outs += [lynx.linear_fp8(X, wq, ws) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(Y.view(torch.int16), ref) for Y in outs)
+    Y1, Y2 = gu.nan_bf16((M, N)), gu.nan_bf16((M, N))
+    ws1 = torch.empty(lynx.fp8_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for g, Y in zip(graphs, (Y1, Y2)):        # two graphs that share a workspace
+        with torch.cuda.graph(g):
+            lynx.linear_fp8(X, wq, ws, Y=Y, workspace=ws1)
+    for i in range(3):
+        for g, Y in zip(graphs, (Y1, Y2)):
+            Y.view(torch.int16).fill_(gu.NAN_BF16_BITS)
+            ws1.fill_(0xFF)
+            lynx.linear_fp8(X, wq, ws)
+            torch.cuda.synchronize()
+            say(f"fp8 graph replay {i}")
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(Y.view(torch.int16), ref)
