@@ -64,6 +64,9 @@ lynx_status launch_quantize_fp8_weight(const uint16_t* W, int N, int K, uint8_t*
 lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                             const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
                             hipStream_t stream);
+lynx_status launch_gemm_fp8_split(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
+                                  const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
+                                  hipStream_t stream);
 lynx_status launch_block_norm(const lynx_norm& d, hipStream_t stream);
 
 }  // namespace lynx

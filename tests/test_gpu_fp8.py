@@ -140,7 +140,7 @@ def test_quantize_special_values():
     assert ((u8(wq) == codes) | ((codes & 0x7F == 0) & (u8(wq) & 0x7F == 0))).all()
 
 
-@pytest.mark.parametrize("M,N", [(20, 40), (1100, 1000)])
+@pytest.mark.parametrize("M,N", [(20, 40), (1500, 1400), (4300, 4000)])
 def test_non_finite_values_reach_their_row_only(M, N):
     K = 320
     bits, _ = heavy(M, K, 3)
@@ -171,7 +171,8 @@ def test_non_finite_values_reach_their_row_only(M, N):
 SHAPES = [(1, 64, 1), (1, 128, 32), (2, 3072, 640), (16, 192, 17), (17, 320, 33), (31, 576, 130),
           (32, 12288, 64), (33, 64, 65), (64, 448, 200), (65, 1024, 127), (77, 3072, 384), (100, 640, 130),
           (255, 960, 257), (300, 1152, 1000), (1000, 1472, 1102), (4096, 256, 64), (64, 256, 4100),
-          (1024, 64, 1024), (1030, 128, 1100), (1500, 704, 1288), (2048, 192, 1536), (700, 2112, 3000)]
+          (1024, 64, 1024), (1030, 128, 1100), (1500, 704, 1288), (2048, 192, 1536), (700, 2112, 3000),
+          (3000, 64, 1700), (1700, 320, 1291)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -184,7 +185,8 @@ def test_product_shapes(M, K, N):
     check_product(Y, xv, wv, f"product {M}x{K}->{N}")
 
 
-@pytest.mark.parametrize("M,K,N", [(4046, 640, 9100), (9216, 256, 3072), (4096, 3072, 12288)])
+@pytest.mark.parametrize("M,K,N", [(4046, 640, 9100), (9216, 256, 3072), (4096, 3072, 12288),
+                                   (8192, 64, 8192), (5000, 448, 7001)])
 def test_product_large_sampled_rows(M, K, N):
     q, s, xv = operand(M, K, 2)
     wq, ws, wv = weight(N, K, 9)
@@ -196,7 +198,8 @@ def test_product_large_sampled_rows(M, K, N):
     check_product(Y[torch.from_numpy(rows).cuda()], xv[rows], wv, f"product {M}x{K}->{N}")
 
 
-@pytest.mark.parametrize("M,K,N", [(8, 512, 40), (200, 384, 300), (1100, 640, 1030)])
+@pytest.mark.parametrize("M,K,N", [(8, 512, 40), (200, 384, 300), (1100, 640, 1030), (1700, 640, 1290),
+                                   (4100, 192, 4500)])
 def test_product_exact_on_small_integers(M, K, N):
     """Integers in -8..8, unlike powers of two per block: every partial sum is exact in fp32 and
     the result checks lane, channel and scale assignment bit for bit."""
