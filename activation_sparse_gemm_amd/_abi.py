@@ -391,11 +391,13 @@ def linear_fp8(X, Wq, Ws, Y=None, workspace=None):
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     y = _expect(Y, torch.bfloat16, (M, N), dev, "Y")
     if workspace is None:
-        workspace = torch.empty((max(fp8_workspace_bytes(M, K), 1),), dtype=torch.uint8, device=dev)
+        nbytes = fp8_workspace_bytes(M, K)
+        if nbytes > 0:
+            workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: must be a contiguous tensor on {dev}")
-    _call("lynx_linear_fp8", dev, x, wq, ws, y, M, N, K, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    _call("lynx_linear_fp8", dev, x, wq, ws, y, M, N, K, _ptr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
     return Y
 
 

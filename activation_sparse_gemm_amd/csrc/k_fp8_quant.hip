@@ -9,21 +9,8 @@
 namespace lynx {
 namespace {
 
-__device__ __forceinline__ uint32_t amax8(const u32x4& v) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((v[i] << 16) & 0x7FFF0000u, v[i] & 0x7FFF0000u));
-    return m;  // fp32 bits of the largest |x|
-}
-
-__device__ __forceinline__ u32x2 quant8(const u32x4& v, float inv) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(v[i] << 16) * inv;
-        f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u) * inv;
-    }
-    return u32x2{fp8_pack4(f[0], f[1], f[2], f[3]), fp8_pack4(f[4], f[5], f[6], f[7])};
+__device__ __forceinline__ u32x2 quant8(const u32x4& v, float divisor) {
+    return u32x2{fp8_pack4(v[0], v[1], divisor), fp8_pack4(v[2], v[3], divisor)};
 }
 
 // Activations.  A wave takes 512 channels (one scale word) of U consecutive
@@ -51,8 +38,8 @@ __global__ __launch_bounds__(256) void quantize_fp8_kernel(const uint16_t* __res
     uint32_t mine = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const uint32_t byte = fp8_scale_byte(row16_max(amax8(v[u])));
-        const u32x2 w = quant8(v[u], fp8_inverse(byte));
+        const uint32_t byte = fp8_scale_byte(row16_max(fp8_amax8(v[u])));
+        const u32x2 w = quant8(v[u], fp8_divisor(byte));
         if (in && row0 + u < M)
             *reinterpret_cast<u32x2*>(q + size_t(row0 + u) * size_t(K) + c) = w;
         const uint32_t sw = fp8_scale_word(byte);
@@ -82,7 +69,7 @@ __global__ __launch_bounds__(256) void quantize_fp8_weight_kernel(const uint16_t
             v[j] = *reinterpret_cast<const u32x4*>(W + size_t(r0 + 16 * j) * size_t(K) + c);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, amax8(v[j]));
+    for (int j = 0; j < 8; ++j) m = max(m, fp8_amax8(v[j]));
     m = row16_max(m);
     m = max(max(uint32_t(__builtin_amdgcn_readlane(int(m), 0)),
                 uint32_t(__builtin_amdgcn_readlane(int(m), 16))),
@@ -91,11 +78,11 @@ __global__ __launch_bounds__(256) void quantize_fp8_weight_kernel(const uint16_t
     if ((t & 63) == 0) part[t >> 6] = m;
     __syncthreads();
     const uint32_t byte = fp8_scale_byte(max(max(part[0], part[1]), max(part[2], part[3])));
-    const float inv = fp8_inverse(byte);
+    const float div = fp8_divisor(byte);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (in && r0 + 16 * j < N)
-            *reinterpret_cast<u32x2*>(q + size_t(r0 + 16 * j) * size_t(K) + c) = quant8(v[j], inv);
+            *reinterpret_cast<u32x2*>(q + size_t(r0 + 16 * j) * size_t(K) + c) = quant8(v[j], div);
     // the last block of a row also fills the unused places of its last word
     const int n = kb == blocks - 1 ? pitch - kb : 1;
     if (t < n) scale[size_t(nb) * size_t(pitch) + kb + t] = uint8_t(t == 0 ? byte : kScaleOne);

@@ -1,6 +1,6 @@
 // Tiled 8-bit GEMM: Y = sum over K blocks of 2^(ex + ew) (Xq Wq^T), e4m3
 // operands with E8M0 block scales, bf16 out (lynx.h).  The instruction and its
-// rounding are described in k_gemm_fp8_split.hip.
+// rounding are described in k_gemm_fp8_few.hip.
 //
 // Persistent workgroups of 4 waves walk tiles of 64 NA x 64 NB, each wave
 // 32 NA x 32 NB of it as NA x NB accumulators of 32 x 32 (matrix operand A = W,
@@ -355,9 +355,12 @@ lynx_status launch_tiled(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq
 lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                             const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
                             hipStream_t stream) {
-    if (M <= 64) return launch_gemm_fp8_split(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
+    if (M <= kFewRows) return launch_gemm_fp8_few(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
     int cus = 0;
     if (device_cu_count(&cus) != LYNX_OK) return LYNX_ERR_DEVICE;
+    bool taken = false;
+    const lynx_status st = launch_gemm_fp8_mid(Xq, Xs, Wq, Ws, Y, M, N, K, cus, &taken, stream);
+    if (taken) return st;
     // Rounds of tiles over the compute units, each at its tile's time relative to a
     // 256 x 256 one (measured at K = 3072: 33 us; 256 x 192 0.83 of that; 128 x 128, two
     // workgroups a unit, 0.75, 0.45 with at most one).  4096 x 9216: 256 x 192 101 us,
@@ -367,7 +370,6 @@ lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t*
     const long wide = rounds(tiles(256, 256), cus) * 100, mid = rounds(tiles(256, 192), cus) * 83;
     const long t22 = tiles(128, 128);
     const long small = t22 <= cus ? 45 : rounds(t22, 2 * cus) * 75;
-    if (t22 < cus / 4) return launch_gemm_fp8_split(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
     if (small < wide && small < mid)
         return launch_tiled<2, 2>(Xq, Xs, Wq, Ws, Y, M, N, K, cus, stream);
     return mid < wide ? launch_tiled<4, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, cus, stream)

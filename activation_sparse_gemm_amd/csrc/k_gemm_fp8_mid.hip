@@ -1,0 +1,204 @@
+// 8-bit GEMM for a middling number of output tiles: too few 128 x 128 tiles to
+// fill the chip, more rows than the K-split kernel's registers serve well.
+//
+// A workgroup of KG groups of 4 waves takes one tile of 32 RM x 32 CN outputs; group
+// g takes the K blocks g, g + KG, ...  A step is KG blocks: 128-byte rows of X and W
+// (swizzled) and the rows' scale words, moved by DMA into a ring of SLOTS slots, so
+// that SLOTS - 1 steps are in flight: such a tile's arithmetic is short, and what
+// bounds it is how many bytes a compute unit keeps under way.  Per step a wait, a
+// barrier, the next loads, 2 (RM + CN) LDS reads and RM CN
+// v_mfma_scale_f32_16x16x128_f8f6f4 a wave (matrix operand A = W, B = X; lane l, r =
+// l % 16, q = l / 16: row r of each, 16-byte chunks q and 4 + q of a block; D: row r of
+// X, rows 4 q .. 4 q + 3 of W).  Channels past K are loaded again from inside the row:
+// the upper half of a last block of 64 is zeroed in W, blocks that fill up a step are
+// weighted 2^-127 in both operands, whose products are zero in fp32.  (A lane's
+// scale is not that of the lane's own channels but of a 32-channel piece of the
+// instruction's, so scales cannot mask half a block here.)  The groups' sums are
+// joined through LDS in order.
+#include "lynx_fp8.h"
+#include "lynx_tile.h"
+
+namespace lynx {
+namespace {
+
+template <int RM, int CN, int KG, int SLOTS>
+__global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
+    const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
+    const uint8_t* __restrict__ Wq, const uint32_t* __restrict__ Ws, uint16_t* __restrict__ Y,
+    int M, int N, int K) {
+    constexpr int TM = 32 * RM, TN = 32 * CN;       // waves 2 x 2 of 16 RM x 16 CN
+    constexpr int kX = TM * 128, kW = TN * 128;
+    constexpr int kGroup = kX + kW + 1024;          // one block: + a scale word per row of X
+    constexpr int kSlot = KG * kGroup;
+    constexpr int kDmaX = RM, kDmaW = CN, kDma = kDmaX + kDmaW + 1;  // per wave and step
+    constexpr int kJoin = (KG - 1) * TM * TN * 4;
+    static_assert(TM <= 256 && SLOTS * kSlot <= 160 * 1024 && kJoin <= SLOTS * kSlot, "LDS budget");
+    static_assert((SLOTS - 2) * kDma < 64, "vmcnt range");
+    __shared__ __attribute__((aligned(1024))) char smem[SLOTS * kSlot];
+
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int wave = wid & 3, group = wid >> 2;
+    const int r = lane & 15, q = lane >> 4;
+    const int wm = wave & 1, wn = wave >> 1;
+    const int tiles_m = (M + TM - 1) / TM, tiles_n = (N + TN - 1) / TN;
+    int tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int blocks = (K + kFp8Block - 1) / kFp8Block;
+    const int steps = (blocks + KG - 1) / KG;
+    const int words = fp8_scale_words(K);
+    const int nblocks = (N + kFp8Block - 1) / kFp8Block;
+
+    const uint32_t lds0 = lds_addr(smem) + uint32_t(group * kGroup);
+    const i32x4 rsX = make_rsrc(Xq, uint32_t(M) * uint32_t(K));
+    const i32x4 rsW = make_rsrc(Wq, uint32_t(N) * uint32_t(K));
+    const i32x4 rsS = make_rsrc(Xs, uint32_t(words) * uint32_t(M) * 4u);
+    // DMA instruction j of wave w moves rows 8 w + l/8 + 32 j, lane l's 16 bytes the
+    // chunk that the row's swizzle puts there (the same for every j)
+    const int lrow = 8 * wave + (lane >> 3);
+    const int chunk = (lane & 7) ^ swz128(lrow);
+    const uint32_t vx = uint32_t(tm * TM + lrow) * uint32_t(K) + uint32_t(16 * chunk);
+    const uint32_t vw = uint32_t(tn * TN + lrow) * uint32_t(K) + uint32_t(16 * chunk);
+    // rows past the end take the last row's words (the word's offset is not range checked)
+    const uint32_t vs = uint32_t(min(tm * TM + (64 * wave) % TM + lane, M - 1)) * 4u;
+    auto load = [&](int step, int slot) {  // past the last step: the last block again
+        const uint32_t base = lds0 + uint32_t(slot * kSlot);
+        const int kb = min(step * KG + group, blocks - 1);
+        const uint32_t back = kb * kFp8Block + 64 < K || chunk < 4 ? 0u : 64u;
+        const uint32_t off = uint32_t(kb) * kFp8Block;
+#pragma unroll
+        for (int j = 0; j < kDmaX; ++j)
+            dma16(base + 1024 * (wave + 4 * j), vx - back + uint32_t(32 * j) * uint32_t(K), rsX, off);
+#pragma unroll
+        for (int j = 0; j < kDmaW; ++j)
+            dma16(base + kX + 1024 * (wave + 4 * j), vw - back + uint32_t(32 * j) * uint32_t(K), rsW,
+                  off);
+        dma4(base + kX + kW + 256 * wave, vs, rsS, uint32_t(kb >> 2) * uint32_t(M) * 4u);
+    };
+#pragma unroll
+    for (int s = 0; s < SLOTS - 1; ++s) load(s, s);
+
+    static_assert(128 % (16 * CN) == 0, "a wave's columns lie in one scale block of W");
+    const int row0 = tm * TM + wm * 16 * RM, col0 = tn * TN + wn * 16 * CN;
+    const uint32_t* wsp = Ws + size_t(__builtin_amdgcn_readfirstlane(
+                                   min(col0 / kFp8Block, nblocks - 1))) * size_t(words);
+    const int sw = swz128(r);
+    const int offX = group * kGroup + (wm * 16 * RM + r) * 128;
+    const int offW = group * kGroup + kX + (wn * 16 * CN + r) * 128;
+    const int offS = group * kGroup + kX + kW + (wm * 16 * RM + r) * 4;
+    f32x4 acc[RM][CN];
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < CN; ++j) acc[i][j] = f32x4{};
+
+    int slot = 0;
+    for (int step = 0; step < steps; ++step) {
+        const int kb = step * KG + group;
+        const uint32_t ws = wsp[min(kb >> 2, words - 1)];
+        wait_vmcnt_lgkm0<(SLOTS - 2) * kDma>();  // this step has landed, the last one's reads are done
+        block_barrier();
+        load(step + SLOTS - 1, slot == 0 ? SLOTS - 1 : slot - 1);
+        const char* s = smem + slot * kSlot;
+        const int shift = 8 * (kb & 3);
+        const uint32_t keep = kb < blocks ? 0xFFu : 0u;
+        const bool upper = kb * kFp8Block + 64 < K;
+        i32x8 x[RM], w[CN];
+        uint32_t sx[RM];
+        auto frag = [&](int off, bool both) {
+            const i32x4 lo = lds_read<i32x4>(s, off + 16 * (q ^ sw));
+            const i32x4 hi = lds_read<i32x4>(s, off + 16 * ((4 + q) ^ sw));
+            return __builtin_shufflevector(lo, both ? hi : i32x4{}, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+#pragma unroll
+        for (int i = 0; i < RM; ++i) x[i] = frag(offX + i * 16 * 128, true);
+#pragma unroll
+        for (int j = 0; j < CN; ++j) w[j] = frag(offW + j * 16 * 128, upper);
+#pragma unroll
+        for (int i = 0; i < RM; ++i) sx[i] = (lds_read<uint32_t>(s, offS + i * 64) >> shift) & keep;
+        const uint32_t sws = (ws >> shift) & keep;
+#pragma unroll
+        for (int i = 0; i < RM; ++i)
+#pragma unroll
+            for (int j = 0; j < CN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    w[j], x[i], acc[i][j], 0, 0, 0, int(sws), 0, int(sx[i]));
+        slot = slot == SLOTS - 1 ? 0 : slot + 1;
+    }
+    wait_vmcnt_lgkm0<0>();  // the loads past the last step write LDS too
+    block_barrier();
+    if constexpr (KG > 1) {
+        f32x4* join = reinterpret_cast<f32x4*>(smem);
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int j = 0; j < CN; ++j)
+                    join[(((group - 1) * 4 + wave) * RM * CN + i * CN + j) * 64 + lane] = acc[i][j];
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int j = 0; j < CN; ++j)
+                    acc[i][j] += join[((g * 4 + wave) * RM * CN + i * CN + j) * 64 + lane];
+    }
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+        const int m = row0 + 16 * i + r;
+        if (m >= M) continue;
+        uint16_t* y = Y + size_t(m) * size_t(N);
+#pragma unroll
+        for (int j = 0; j < CN; ++j) {
+            const int n = col0 + 16 * j + 4 * q;
+            const f32x4& v = acc[i][j];
+            if ((N & 3) == 0) {  // then a group of 4 columns is inside N or outside
+                if (n < N)
+                    *reinterpret_cast<u32x2*>(y + n) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            } else if ((N & 1) == 0) {
+                if (n < N) *reinterpret_cast<uint32_t*>(y + n) = pack_bf16x2(v[0], v[1]);
+                if (n + 2 < N) *reinterpret_cast<uint32_t*>(y + n + 2) = pack_bf16x2(v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < N)
+                        y[n + e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[e]));
+            }
+        }
+    }
+}
+
+template <int RM, int CN, int KG, int SLOTS>
+lynx_status launch_mid(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws,
+                       uint16_t* Y, int M, int N, int K, hipStream_t stream) {
+    const long tiles = long((M + 32 * RM - 1) / (32 * RM)) * ((N + 32 * CN - 1) / (32 * CN));
+    hipLaunchKernelGGL((gemm_fp8_mid<RM, CN, KG, SLOTS>), dim3(unsigned(tiles)), dim3(256 * KG), 0,
+                       stream, Xq, Xs, Wq, reinterpret_cast<const uint32_t*>(Ws), Y, M, N, K);
+    return launch_status();
+}
+
+}  // namespace
+
+lynx_status launch_gemm_fp8_mid(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
+                                const uint8_t* Ws, uint16_t* Y, int M, int N, int K, int cus,
+                                bool* taken, hipStream_t stream) {
+    // The largest tile that still gives most compute units one (two where two
+    // workgroups fit a unit); small tiles split K over more groups instead.  At
+    // K = 3072, us: 64 x 9216 32x32 11.6, 32x64 8.5; 128 x 3072 10.1 and 6.9; 4096 x 64
+    // 5.8 and 6.7; 200 x 9216 32x128 14.3, 32x64 18.1; 512 x 3072 128x64 11.5, 32x128
+    // 13.4, the tiled kernel's 128x128 14.1.
+    auto tiles = [&](int tm, int tn) { return long((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+    *taken = true;
+    if (tiles(32, 32) <= cus) return launch_mid<1, 1, 4, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
+    if (tiles(32, 64) <= 2 * cus) return launch_mid<1, 2, 2, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
+    if (tiles(128, 64) <= cus) return launch_mid<4, 2, 2, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
+    if (tiles(32, 128) <= 2 * cus) return launch_mid<1, 4, 1, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
+    *taken = false;
+    return LYNX_OK;
+}
+
+}  // namespace lynx

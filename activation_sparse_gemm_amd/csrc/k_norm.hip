@@ -203,12 +203,11 @@ __global__ __launch_bounds__(256) void block_norm_kernel(const NormArgs A) {
             for (int j = 0; j < 8; ++j)
                 m = max(m, in[i] ? __float_as_uint(v[i].f[j]) & 0x7FFFFFFFu : 0u);
             const uint32_t byte = fp8_scale_byte(row16_max(m));
-            const float inv = fp8_inverse(byte);
+            const float div = fp8_divisor(byte);
             const float* f = v[i].f;
             if (in[i])
                 *reinterpret_cast<u32x2*>(A.q + base + c[i]) =
-                    u32x2{fp8_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                          fp8_pack4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
+                    u32x2{fp8_pack4(f[0], f[1], f[2], f[3], div), fp8_pack4(f[4], f[5], f[6], f[7], div)};
             const int word = i * W + wave;
             const uint32_t sw = fp8_scale_word(byte);
             if (lane == 0 && 512 * word < A.C) A.q_scale[size_t(word) * size_t(A.M) + row] = sw;

@@ -36,16 +36,36 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax) {
     return amax >= 0x7F800000u ? kScaleNaN : b;
 }
 
-// 2^-e for a scale byte of fp8_scale_byte (e <= 120, so it is a normal
-// number); 0 for the NaN scale, whose values do not matter.
-__device__ __forceinline__ float fp8_inverse(uint32_t byte) {
-    return byte == kScaleNaN ? 0.f : __uint_as_float((254u - byte) << 23);
+// The fp32 number that the conversions below divide by for a scale byte: they use
+// its exponent field alone.  (255, the NaN scale, gives values that do not matter.)
+__device__ __forceinline__ float fp8_divisor(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// four values to e4m3 bytes, divided by 2^e (exactly) and rounded to nearest even
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d, float divisor) {
+    typedef short i16x2 __attribute__((ext_vector_type(2)));
+    i16x2 w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, divisor, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, divisor, true);
+    return __builtin_bit_cast(uint32_t, w);
+}
+// the same from two words of bf16 pairs
+__device__ __forceinline__ uint32_t fp8_pack4(uint32_t ab, uint32_t cd, float divisor) {
+    typedef short i16x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    i16x2 w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(bf16x2, ab), divisor, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(bf16x2, cd), divisor, true);
+    return __builtin_bit_cast(uint32_t, w);
 }
 
-// four values, already divided by their scale (|v| <= 448), to e4m3 bytes
-__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+// fp32 bits of the largest magnitude of eight bf16
+__device__ __forceinline__ uint32_t fp8_amax8(const u32x4& v) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7FFF7FFFu));
+    return uint32_t(m[0] > m[1] ? m[0] : m[1]) << 16;
 }
 
 // The wave's scale word from the bytes of its four 16-lane groups (uniform).
@@ -64,9 +84,19 @@ lynx_status launch_quantize_fp8_weight(const uint16_t* W, int N, int K, uint8_t*
 lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                             const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
                             hipStream_t stream);
-lynx_status launch_gemm_fp8_split(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
-                                  const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
-                                  hipStream_t stream);
+
+// Product kernels (launch_gemm_fp8 chooses).  _few: M <= kFewRows, from the 8-bit
+// operand, or from bf16 X quantised on the way in (Xs == nullptr).
+constexpr int kFewRows = 16;
+constexpr int kFewQuant = 32768;  // and at most so many elements of X
+inline bool fp8_few_quant(int64_t M, int64_t K) { return M <= kFewRows && M * K <= kFewQuant; }
+lynx_status launch_gemm_fp8_few(const void* X, const uint8_t* Xs, const uint8_t* Wq,
+                                const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
+                                hipStream_t stream);
+// Takes the problem if its tile counts suit it; *taken says whether it did.
+lynx_status launch_gemm_fp8_mid(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
+                                const uint8_t* Ws, uint16_t* Y, int M, int N, int K, int cus,
+                                bool* taken, hipStream_t stream);
 lynx_status launch_block_norm(const lynx_norm& d, hipStream_t stream);
 
 }  // namespace lynx

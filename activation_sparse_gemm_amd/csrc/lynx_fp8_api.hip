@@ -13,7 +13,8 @@ struct Fp8Layout {
 };
 
 Fp8Layout fp8_layout(int64_t M, int64_t K) {
-    Fp8Layout L;
+    Fp8Layout L = {0, 0, 0};
+    if (fp8_few_quant(M, K)) return L;  // quantised inside the product
     L.q = 0;
     L.scale = round_up256(size_t(M) * size_t(K));
     L.total = L.scale + round_up256(size_t(fp8_scale_words(int(K))) * size_t(M) * 4);
@@ -109,11 +110,16 @@ lynx_status lynx_linear_fp8(const uint16_t* X, const uint8_t* Wq, const uint8_t*
     if (!X || !Wq || !Ws || !Y) return LYNX_ERR_NULL;
     if (!all16({X, Wq, Ws, Y})) return LYNX_ERR_ALIGN;
     const Fp8Layout L = fp8_layout(M, K);
-    if (!workspace || workspace_bytes < L.total) return LYNX_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LYNX_ERR_ALIGN;
+    if (L.total > 0) {
+        if (!workspace || workspace_bytes < L.total) return LYNX_ERR_WORKSPACE;
+        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LYNX_ERR_ALIGN;
+    }
     lynx_status st = check_device();
     if (st != LYNX_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (L.total == 0)
+        return debug_sync(
+            launch_gemm_fp8_few(X, nullptr, Wq, Ws, Y, int(M), int(N), int(K), s), s);
     uint8_t* q = static_cast<uint8_t*>(workspace) + L.q;
     uint8_t* scale = static_cast<uint8_t*>(workspace) + L.scale;
     st = launch_quantize_fp8(X, int(M), int(K), q, scale, s);

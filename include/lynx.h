@@ -266,7 +266,8 @@ lynx_status lynx_quantize_fp8_weight(const uint16_t* W, int64_t N, int64_t K, ui
 
 /*
  * Bytes of device workspace lynx_linear_fp8 needs for an (M, K) activation: its
- * values and scales, each 256-byte aligned.  Returns 0 for invalid sizes.
+ * values and scales, each 256-byte aligned; 0 where it needs none (a few rows,
+ * M <= 16 and M K <= 32768, are quantised inside the product) and for invalid sizes.
  */
 size_t lynx_fp8_workspace_bytes(int64_t M, int64_t K);
 
@@ -274,7 +275,7 @@ size_t lynx_fp8_workspace_bytes(int64_t M, int64_t K);
  * The whole layer: quantises X into `workspace`, then the product.
  * Inputs: X [M][K] bf16; Wq, Ws a quantised weight [N][K].  Output: Y [M][N] bf16.
  * workspace: >= lynx_fp8_workspace_bytes(M, K) bytes, 256-byte aligned, contents
- * on entry irrelevant, clobbered.
+ * on entry irrelevant, clobbered; NULL is allowed where that is 0.
  */
 lynx_status lynx_linear_fp8(const uint16_t* X, const uint8_t* Wq, const uint8_t* Ws, uint16_t* Y,
                             int64_t M, int64_t N, int64_t K, void* workspace,

@@ -26,7 +26,10 @@ def test_quantize_validation(fn, kw, status):
 
 
 def test_workspace_bytes():
-    assert _abi.fp8_workspace_bytes(16, 128) == 16 * 128 + 256
+    assert _abi.fp8_workspace_bytes(17, 128) == 2304 + 256
+    assert _abi.fp8_workspace_bytes(16, 2112) == 33792 + 512
+    # few rows are quantised inside the product
+    assert _abi.fp8_workspace_bytes(16, 2048) == 0 and _abi.fp8_workspace_bytes(1, 12288) == 0
     # 333 x 1472: values rounded up to 256, three scale words a row
     assert _abi.fp8_workspace_bytes(333, 1472) == 490240 + 4096
     assert _abi.fp8_workspace_bytes(333, 1472) >= 333 * 1472 + 3 * 333 * 4
@@ -38,7 +41,8 @@ def test_workspace_bytes():
     (dict(K=96), SHAPE), (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(M=1 << 20, N=1 << 12), SHAPE),
     (dict(x=None), NULL), (dict(wq=None), NULL), (dict(ws=None), NULL), (dict(y=None), NULL),
     (dict(x=A + 1), ALIGN), (dict(wq=A + 8), ALIGN), (dict(ws=A + 4), ALIGN), (dict(y=A + 2), ALIGN),
-    (dict(ws_=None), WORKSPACE), (dict(n=16 * 128 + 255), WORKSPACE), (dict(ws_=B + 16), ALIGN),
+    (dict(M=17, ws_=None), WORKSPACE), (dict(M=17, n=2304 + 255), WORKSPACE),
+    (dict(M=17, ws_=B + 16), ALIGN),
     (dict(M=0), OK), (dict(N=0), OK),
 ])
 def test_linear_validation(kw, status):

@@ -168,7 +168,10 @@ def test_non_finite_values_reach_their_row_only(M, N):
 
 # ---- the product -------------------------------------------------------------------
 
-SHAPES = [(1, 64, 1), (1, 128, 32), (2, 3072, 640), (16, 192, 17), (17, 320, 33), (31, 576, 130),
+# every kernel: M <= 16; 32x32, 32x64, 128x64 and 32x128 tiles of a split K; 128x128,
+# 256x192 and 256x256 tiles; each with ragged rows and columns, N % 8, N % 4, N % 2 == 0 and
+# odd N, K % 128 == 64 and K below the ring depth (unlike block scales show a wrong one)
+SHAPES = [(9, 3072, 8200), (16, 64, 9001), (190, 704, 9100), (190, 64, 9101), (500, 832, 2050), (1, 64, 1), (1, 128, 32), (2, 3072, 640), (16, 192, 17), (17, 320, 33), (31, 576, 130),
           (32, 12288, 64), (33, 64, 65), (64, 448, 200), (65, 1024, 127), (77, 3072, 384), (100, 640, 130),
           (255, 960, 257), (300, 1152, 1000), (1000, 1472, 1102), (4096, 256, 64), (64, 256, 4100),
           (1024, 64, 1024), (1030, 128, 1100), (1500, 704, 1288), (2048, 192, 1536), (700, 2112, 3000),
@@ -253,7 +256,8 @@ def test_product_extreme_scales():
 
 # ---- the whole layer ---------------------------------------------------------------
 
-@pytest.mark.parametrize("M,K,N", [(1, 64, 40), (2, 3072, 1000), (15, 576, 130), (40, 1472, 70), (300, 640, 520),
+@pytest.mark.parametrize("M,K,N", [(1, 64, 40), (2, 3072, 1000), (15, 576, 130), (16, 2048, 9000), (1, 32768, 40),
+                                   (16, 2112, 8200), (3, 10880, 50), (16, 64, 33), (40, 1472, 70), (300, 640, 520),
                                    (1300, 448, 1100)])
 def test_layer_is_quantiser_then_product(M, K, N):
     bits, x = heavy(M, K, M)
@@ -298,7 +302,7 @@ def test_python_checks_name_the_argument():
         with pytest.raises(err, match=name):
             call()
     with pytest.raises(lynx.LynxError, match="LYNX_ERR_WORKSPACE"):
-        lynx.linear_fp8(X, wq, ws, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        lynx.linear_fp8(dev(heavy(17, 128, 1)[0]), wq, ws, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(lynx.LynxError, match="LYNX_ERR_SHAPE"):
         lynx.quantize_fp8(torch.zeros((2, 96), dtype=torch.bfloat16, device="cuda"))
 
