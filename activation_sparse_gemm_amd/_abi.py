@@ -323,15 +323,25 @@ def _matrix(t, name):
     return t.shape[0], t.shape[1], dev
 
 
+_fns: dict = {}
+
+
 def _call(fn: str, dev: torch.device, *args) -> None:
     """Calls the entry point on `dev`'s current stream, with `dev` as the
-    current device (the library works on the current device)."""
-    f = getattr(lib(), fn)
-    if dev.index == torch.cuda.current_device():
-        _check(f(*args, _stream(dev)), fn)
+    current device (the library works on the current device).  Short calls are
+    bound by this code's time: the stream handle comes without a Stream object
+    around it (0.1 us instead of 2)."""
+    f = _fns.get(fn)
+    if f is None:
+        f = _fns[fn] = getattr(lib(), fn)
+    i = dev.index
+    if i == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, _stream(dev)), fn)
+            st = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != LYNX_OK:
+        raise LynxError(st, fn)
 
 
 def _scale_words(K: int) -> int:
@@ -348,7 +358,7 @@ def quantize_fp8(X: torch.Tensor, out: tuple | None = None):
     M, K, dev = _matrix(X, "X")
     x = _expect(X, torch.bfloat16, (M, K), dev, "X")
     shape = (_scale_words(K), M, 4)
-    q, scale = out if out is not None else (torch.empty((M, K), dtype=FP8, device=dev),
+    q, scale = out if out is not None else (torch.empty(M, K, dtype=FP8, device=dev),
                                             torch.empty(shape, dtype=E8M0, device=dev))
     _call("lynx_quantize_fp8", dev, x, M, K, _expect(q, FP8, (M, K), dev, "q"),
           _expect(scale, E8M0, shape, dev, "scale"))
@@ -365,7 +375,7 @@ def quantize_fp8_weight(W: torch.Tensor, out: tuple | None = None):
     N, K, dev = _matrix(W, "W")
     w = _expect(W, torch.bfloat16, (N, K), dev, "W")
     shape = ((N + 127) // 128, 4 * _scale_words(K))
-    q, scale = out if out is not None else (torch.empty((N, K), dtype=FP8, device=dev),
+    q, scale = out if out is not None else (torch.empty(N, K, dtype=FP8, device=dev),
                                             torch.empty(shape, dtype=E8M0, device=dev))
     _call("lynx_quantize_fp8_weight", dev, w, N, K, _expect(q, FP8, (N, K), dev, "q"),
           _expect(scale, E8M0, shape, dev, "scale"))
@@ -388,7 +398,7 @@ def linear_fp8(X, Wq, Ws, Y=None, workspace=None):
     x = _expect(X, torch.bfloat16, (M, K), dev, "X")
     N, wq, ws = _fp8_weight(Wq, Ws, K, dev)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        Y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     y = _expect(Y, torch.bfloat16, (M, N), dev, "Y")
     if workspace is None:
         nbytes = fp8_workspace_bytes(M, K)
@@ -409,7 +419,7 @@ def linear_fp8_packed(q, scale, Wq, Ws, Y=None):
     xs = _expect(scale, E8M0, (_scale_words(K), M, 4), dev, "scale")
     N, wq, ws = _fp8_weight(Wq, Ws, K, dev)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        Y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     _call("lynx_linear_fp8_packed", dev, xq, xs, wq, ws,
           _expect(Y, torch.bfloat16, (M, N), dev, "Y"), M, N, K)
     return Y
@@ -418,8 +428,6 @@ def linear_fp8_packed(q, scale, Wq, Ws, Y=None):
 def _sample_rows(t, C, dev, name):
     """(pointer, rows, stride) of per-sample parameters [rows, C] (or [C]); the
     rows may lie apart, as in a slice of a modulation projection's output."""
-    if t is None:
-        return None, 1, 0
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
     if t.dim() not in (1, 2) or t.shape[-1] != C:
@@ -436,46 +444,50 @@ def _sample_rows(t, C, dev, name):
 def _block_norm(x, y, gate, post_norm, post_weight, post_bias, post_eps, residual_scale, norm,
                 weight, bias, scale, shift, eps, fp8, x_out, out):
     M, C, dev = _matrix(x, "x")
-    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+    f32 = x.dtype is torch.float32
+    if not f32 and x.dtype is not torch.bfloat16:
         raise TypeError(f"x: expected torch.bfloat16 or torch.float32, got {x.dtype}")
     if norm not in NORM_KINDS or post_norm not in NORM_KINDS:
         raise ValueError(f"a norm is one of {list(NORM_KINDS)}")
-    a = Norm(x=_expect(x, x.dtype, (M, C), dev, "x"), M=M, C=C, samples=1,
-             residual_scale=residual_scale, post_eps=post_eps, eps=eps,
-             x_fp32=x.dtype is torch.float32, post_norm=NORM_KINDS[post_norm],
-             norm=NORM_KINDS[norm])
+    rows, bf16 = (M, C), torch.bfloat16
+    xp, yp, xo = _expect(x, x.dtype, rows, dev, "x"), None, None
     if y is not None:
-        a.y = _expect(y, torch.bfloat16, (M, C), dev, "y")
+        yp = _expect(y, bf16, rows, dev, "y")
         if x_out is None:
             x_out = torch.empty_like(x)
-        a.x_out = _expect(x_out, x.dtype, (M, C), dev, "x_out")
-    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("weight", weight),
-                    ("bias", bias)):
-        if t is not None:
-            setattr(a, name, _expect(t, torch.bfloat16, (C,), dev, name))
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is not None:
-            p, rows, stride = _sample_rows(t, C, dev, name)
-            setattr(a, name, p)
-            setattr(a, name + "_stride", stride)
-            if rows != 1:
-                if a.samples not in (1, rows):
-                    raise ValueError(f"{name}: {rows} samples, and {a.samples} elsewhere")
-                a.samples = rows
+        xo = _expect(x_out, x.dtype, rows, dev, "x_out")
+
+    def channels(t, name):
+        return None if t is None else _expect(t, bf16, (C,), dev, name)
+
+    samples = 1
+    per_sample = []
+    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        p, n, stride = (None, 1, 0) if t is None else _sample_rows(t, C, dev, name)
+        if n != 1:
+            if samples not in (1, n):
+                raise ValueError(f"{name}: {n} samples, and {samples} elsewhere")
+            samples = n
+        per_sample.append((p, stride))
+    (gp, gs), (sp, ss), (hp, hs) = per_sample
+    h = q = q_scale = None
     if norm is None:
         if fp8 or out is not None:
             raise ValueError("without a norm there is no second output")
     elif fp8:
         shape = (_scale_words(C), M, 4)
         if out is None:
-            out = (torch.empty((M, C), dtype=FP8, device=dev),
+            out = (torch.empty(M, C, dtype=FP8, device=dev),
                    torch.empty(shape, dtype=E8M0, device=dev))
-        a.q = _expect(out[0], FP8, (M, C), dev, "q")
-        a.q_scale = _expect(out[1], E8M0, shape, dev, "q_scale")
+        q, q_scale = _expect(out[0], FP8, rows, dev, "q"), _expect(out[1], E8M0, shape, dev, "q_scale")
     else:
         if out is None:
-            out = torch.empty((M, C), dtype=torch.bfloat16, device=dev)
-        a.h = _expect(out, torch.bfloat16, (M, C), dev, "h")
+            out = torch.empty(M, C, dtype=bf16, device=dev)
+        h = _expect(out, bf16, rows, dev, "h")
+    a = Norm(xp, yp, gp, channels(post_weight, "post_weight"), channels(post_bias, "post_bias"),
+             channels(weight, "weight"), channels(bias, "bias"), sp, hp, xo, h, q, q_scale, M, C,
+             samples, gs, ss, hs, residual_scale, post_eps, eps, f32, NORM_KINDS[post_norm],
+             NORM_KINDS[norm])
     _call("lynx_block_norm", dev, ctypes.byref(a))
     return x_out, out
 
