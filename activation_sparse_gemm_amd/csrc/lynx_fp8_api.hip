@@ -27,8 +27,8 @@ bool all16(std::initializer_list<const void*> ps) {
     return true;
 }
 
-constexpr int64_t kMaxNormRows = int64_t(1) << 23;  // a workgroup per row fits a grid
-constexpr int64_t kMaxNormC = 16384;                // 4 waves of 8 x 8 channels a lane
+constexpr int64_t kMaxNormRows = int64_t(1) << 23;
+constexpr int64_t kMaxNormC = 16384;  // 8 waves of 4 x 8 channels a lane
 
 bool kind_ok(int32_t k) {
     return k == LYNX_NORM_NONE || k == LYNX_NORM_RMS || k == LYNX_NORM_LAYER;
