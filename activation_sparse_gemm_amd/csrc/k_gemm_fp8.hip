@@ -1,32 +1,42 @@
 // Tiled 8-bit GEMM: Y = sum over K blocks of 2^(ex + ew) (Xq Wq^T), e4m3
 // operands with E8M0 block scales, bf16 out (lynx.h).  The instruction and its
-// rounding are described in k_gemm_fp8_few.hip.
+// rounding are described in k_gemm_fp8_few.hip; v_mfma_scale_f32_16x16x128_f8f6f4
+// is used here too: under sustained load the board's power sets the clock, and a
+// loop of this instruction alone reaches 3870 TFLOP/s, of the 32x32x64 one (the
+// accumulator read and written for every 64 channels) 3620.
 //
 // Persistent workgroups of 4 waves walk tiles of 64 NA x 64 NB, each wave
-// 32 NA x 32 NB of it as NA x NB accumulators of 32 x 32 (matrix operand A = W,
-// B = X, so that a lane holds runs of a row of Y).  LDS has two slots of one K
-// block each: 128-byte rows of X and W (swizzled; whole cache lines, so that a
-// line is asked for once) and the rows' scale words, moved there by DMA.  A block is
-// two stages of 64 channels, at NA = NB = 4 16 instructions of 64 cycles a wave
-// each.  A stage's fragments are read from LDS into registers during the stage
-// before it (two sets, 32 bytes of a row per lane and accumulator row or column).
-// So the second stage of block p reads from block p + 1's slot and finds block p's
-// slot free: it opens with the block's only barrier, after which block p + 1 has
-// landed for all waves, and begins to load block p + 2 into slot p.  The loads are
-// spread over the instructions of this stage and the first half of the next: in a
-// burst they hold up the wave that issues them (4 instructions' room instead of 22:
-// 10% of the time).
+// 32 NA x 32 NB of it as NI x NJ = 2 NA x 2 NB accumulators of 16 x 16 (matrix
+// operand A = W, B = X, so that a lane holds runs of a row of Y).  LDS has two slots
+// for a K block of X and two for one of W: 128-byte rows (swizzled; whole cache
+// lines, so that a line is asked for once) and the X rows' scale words, moved there
+// by DMA.
 //
-// The blocks run on across tiles: a tile's last two second stages load the next
-// tile's first two blocks, in flight during the epilogue.  A tile has at least two
-// blocks; K <= 128, and a last block of 64 channels, are filled up with channels
-// loaded again, under scales of 2^-127 for both operands, whose products are zero
-// in fp32.
+// A block is NI NJ instructions, W's fragments one after another against all of X's.
+// X's fragments of block p + 1 are read into registers during block p (two sets), W's
+// two ahead of their use (a ring of kRing).  So block p reads X's slot p + 1 and W's
+// slot p, and there are two barriers to a block:
+//   B0 near its start: X of block p + 1 has landed;
+//   B1 before its last two W fragments, which have been read: W of block p + 1 has
+//      landed; W's slot p is free and takes block p + 2, and X's slot p + 1, whose
+//      fragments are all in registers, takes block p + 3 in the next block.
+// A slot's loads have about a block's time (2048 cycles at NA = NB = 4) to land.  They
+// are spread over the block: in a burst they hold up the wave that issues them.
 //
-// Scales: lane l's B operand is row l % 32 of X, its scale the byte of the K block
-// in that row's word (4 blocks); a 32-row piece of W lies in one 128-row scale
-// block, so its scale is uniform and comes through the scalar cache.
+// The blocks run on across tiles: a tile's last two blocks load the next tile's
+// first two, in flight during the epilogue.  256 x 256 tiles (the loop for
+// an odd number of blocks would spill there: 17% at K = 1152, where a block more costs
+// 11) and K <= 128 are filled up to an even number of blocks, and a last block of 64
+// channels to 128, with channels loaded again, under scales of 2^-127 for both
+// operands, whose products are zero in fp32.
+//
+// Scales: the scale of row r = l % 16 and the instruction's channels 32 q .. 32 q + 31
+// comes from lane l = 16 q + r (a lane's own channels are chunks q and 4 + q of 16).
+// X's is the byte of the K block in the row's word (4 blocks); a 16-row piece of W
+// lies in one 128-row scale block, so its scale is uniform and comes through the
+// scalar cache.
 #include <type_traits>
+#include <utility>
 
 #include "lynx_fp8.h"
 #include "lynx_tile.h"
@@ -34,47 +44,57 @@
 namespace lynx {
 namespace {
 
-typedef uint32_t lds_u32x2 __attribute__((ext_vector_type(2)));
+// Instructions from .. to - 1 of a block after which no W fragment is read
+constexpr int spare(int NI, int from, int to) {
+    int n = 0;
+    for (int k = from; k < to; ++k) n += k % NI != 2 && k % NI != 3;
+    return n;
+}
 
-// 32-column blocks that an epilogue turns at a time: 2, or 1 where NB is odd or LDS
-// is shared by two workgroups
-constexpr int epilogue_blocks(int NA, int NB) { return NA == 4 && NB % 2 == 0 ? 2 : 1; }
+// f(0), ..., f(N - 1) with compile-time arguments
+template <typename F, int... I>
+__device__ __forceinline__ void for_each(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
 
-// Epilogue of one wave, N % 8 == 0: 32 rows x 32 CB columns at a time are rounded,
-// turned through the wave's own LDS (`ep`) and stored as whole rows, 16 bytes a
-// lane: CB = 2 writes full 128-byte lines.  Lane l, r = l % 32, h = l / 32, holds of
-// accumulator (a, b) row 32 a + r, columns 32 b + 8 (e / 4) + 4 h + e % 4.  16-byte
-// chunks are swizzled by the row, so that neither side has bank conflicts.  Rows
-// past M and columns past N are sent past the end of the buffer, which drops them;
-// every call issues NA NB 2 stores.
+// Bytes a wave's epilogue turns at a time: 32 rows of 64 columns, or of 32 where the
+// column count or the LDS (shared by two workgroups) does not allow it
+constexpr int epilogue_columns(int NA, int NB) { return NA == 4 && NB % 2 == 0 ? 64 : 32; }
+
+// Epilogue of one wave, N % 8 == 0: 32 rows at a time are rounded, turned through the
+// wave's own LDS (`ep`) and stored as pieces of rows, 16 bytes a lane: 64 columns
+// are full 128-byte lines.  Lane l, r = l % 16, q = l / 16, holds of accumulator (i, j)
+// row 16 i + r, columns 16 j + 4 q .. + 3.  16-byte chunks are swizzled by the row, so
+// that neither side has bank conflicts.  Rows past M and columns past N are sent past
+// the end of the buffer, which drops them; every call issues 2 NA NB stores.
 template <int NA, int NB>
-__device__ __forceinline__ void store_block_rows(const f32x16 (&acc)[NA][NB],
+__device__ __forceinline__ void store_block_rows(const f32x4 (&acc)[2 * NA][2 * NB],
                                                  __amdgpu_buffer_rsrc_t rsY, int N, int row0,
                                                  int col0, char* ep) {
-    constexpr int CB = epilogue_blocks(NA, NB);
-    constexpr int kChunks = 4 * CB, kPitch = 16 * kChunks, kRows = 64 / kChunks;
+    constexpr int kCols = epilogue_columns(NA, NB);
+    constexpr int kChunks = kCols / 8, kPitch = 2 * kCols, kRows = 64 / kChunks;
     const int l = fresh_lane();
-    const int r = l & 31, h = l >> 5;
-    auto swz = [](int row) { return CB == 2 ? row & 7 : (row >> 1) & 3; };
+    const int r = l & 15, q = l >> 4;
+    auto swz = [](int row) { return kCols == 64 ? row & 7 : (row >> 1) & 3; };
     const int orow = l / kChunks, och = l % kChunks;
 #pragma unroll
     for (int a = 0; a < NA; ++a)
 #pragma unroll
-        for (int bp = 0; bp < NB / CB; ++bp) {
+        for (int c = 0; c < 32 * NB / kCols; ++c) {
 #pragma unroll
-            for (int b = 0; b < CB; ++b)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x16& v = acc[a][bp * CB + b];
-                    *reinterpret_cast<lds_u32x2*>(ep + r * kPitch + 16 * ((4 * b + g) ^ swz(r)) +
-                                                  8 * h) =
-                        lds_u32x2{pack_bf16x2(v[4 * g], v[4 * g + 1]),
-                                  pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
+                for (int j = 0; j < kCols / 16; ++j) {
+                    const f32x4& v = acc[2 * a + i][c * (kCols / 16) + j];
+                    const int row = 16 * i + r;
+                    *reinterpret_cast<u32x2*>(ep + row * kPitch +
+                                              16 * ((2 * j + (q >> 1)) ^ swz(row)) + 8 * (q & 1)) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                 }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-            const int col = col0 + 32 * CB * bp + 8 * och;
+            const int col = col0 + kCols * c + 8 * och;
 #pragma unroll
             for (int i = 0; i < 32 / kRows; ++i) {
                 const int lr = i * kRows + orow;
@@ -91,62 +111,66 @@ __device__ __forceinline__ void store_block_rows(const f32x16 (&acc)[NA][NB],
 
 // Epilogue for other N: every lane stores its values one by one.
 template <int NA, int NB>
-__device__ __forceinline__ void store_block_single(const f32x16 (&acc)[NA][NB],
+__device__ __forceinline__ void store_block_single(const f32x4 (&acc)[2 * NA][2 * NB],
                                                    __amdgpu_buffer_rsrc_t rsY, int N, int row0,
                                                    int col0) {
     const int l = fresh_lane();
-    const int r = l & 31, h = l >> 5;
+    const int r = l & 15, q = l >> 4;
 #pragma unroll
-    for (int a = 0; a < NA; ++a)
+    for (int i = 0; i < 2 * NA; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int j = 0; j < 2 * NB; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int col = col0 + 32 * b + 8 * (e / 4) + 4 * h + e % 4;
-                const uint32_t o = (uint32_t(row0 + 32 * a + r) * uint32_t(N) + uint32_t(col)) * 2u;
+            for (int e = 0; e < 4; ++e) {
+                const int col = col0 + 16 * j + 4 * q + e;
+                const uint32_t o = (uint32_t(row0 + 16 * i + r) * uint32_t(N) + uint32_t(col)) * 2u;
                 __builtin_amdgcn_raw_buffer_store_b16(
-                    __builtin_bit_cast(uint16_t, static_cast<__bf16>(acc[a][b][e])), rsY,
+                    __builtin_bit_cast(uint16_t, static_cast<__bf16>(acc[i][j][e])), rsY,
                     col < N ? o : 0xFFFFFFF0u, 0, 0);
             }
 }
 
-// VEC: N % 8 == 0 (two kernels rather than a branch before the epilogue, into whose
-// arms the compiler would move the last stage's instructions)
-template <int NA, int NB, bool VEC>
+// VEC: N % 8 == 0; ODD: a tile has an odd number of blocks, at least 3 (else an even
+// number).  Kernels of their own rather than branches, into whose arms the compiler
+// would move the instructions of the block before.
+template <int NA, int NB, bool VEC, bool ODD>
 __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
     const uint8_t* __restrict__ Wq, const uint32_t* __restrict__ Ws, uint16_t* __restrict__ Y,
     int M, int N, int K) {
     constexpr int TM = 64 * NA, TN = 64 * NB;
+    constexpr int NI = 2 * NA, NJ = 2 * NB;         // accumulators per wave
     constexpr int kRow = 128;                       // LDS bytes per row and block
-    constexpr int kX = TM * kRow, kW = TN * kRow;
-    constexpr int kSlot = kX + kW + 1024;           // + a scale word per row (256 places)
-    constexpr int kDmaX = 2 * NA, kDmaW = 2 * NB;   // DMA instructions per wave and block
-    constexpr int kDma = kDmaX + kDmaW + 1;
-    constexpr int kM = NA * NB;                     // matrix instructions per wave and stage
-    constexpr int kReads = 2 * (NA + NB);           // 16-byte LDS reads per wave and stage
-    constexpr int kBar = kM >= 12 ? 1 : 0;          // the barrier follows instruction kBar
-    constexpr int kTail = kM / 8;                   // instructions after the last LDS read
-    constexpr int kLoad1 = kDma * 3 / 5;            // loads issued in a block's second stage,
-    constexpr int kGaps0 = kM / 2;                  // the others here, early in the next
+    constexpr int kX = TM * kRow + 1024;            // a slot of X: + a scale word per row (256 places)
+    constexpr int kW = TN * kRow;                   // a slot of W
+    constexpr int kDmaX = 2 * NA + 1, kDmaW = 2 * NB;  // DMA instructions per wave and block
+    constexpr int kRing = NB == 3 ? 3 : 4;          // W fragments in registers; divides NJ
+    constexpr int kM = NI * NJ;                     // matrix instructions per wave and block
+    constexpr int kB0 = kM >= 64 ? 8 : 1, kB1 = (NJ - 2) * NI + 1; // the barriers follow these instructions
+    constexpr int kRead = (NJ - 3) * NI + 1;        // X is read before this one
+    constexpr int kTailW = kDmaW / 2;               // loads of W issued after B1, the others next
+    constexpr int kLateW = kM >= 64 ? 13 : 6;       // ... before this instruction
+    constexpr int kEndX = kM >= 64 ? 40 : kM >= 48 ? 24 : kB1;  // X's loads are issued before this one
     constexpr int kStores = 2 * NA * NB;            // stores of an epilogue, at least
-    constexpr int kEp = 2048 * epilogue_blocks(NA, NB);  // a wave's LDS for the epilogue
+    constexpr int kEp = 64 * epilogue_columns(NA, NB);  // a wave's LDS for the epilogue
     constexpr int kBS = NB == 3 ? NB : 1;           // scale blocks a wave's columns touch
     // past the end of X and W (they hold less than 2^31 bytes, and a tile's rows
     // span less than 2^31: kPast plus a row's offset does not wrap)
     constexpr uint32_t kPast = 0x80000000u;
-    static_assert(2 * kSlot + 4 * kEp <= 160 * 1024 / (NA == 4 ? 1 : 2), "LDS budget");
-    static_assert(kStores < 64, "vmcnt range");
-    __shared__ __attribute__((aligned(1024))) char smem[2 * kSlot + 4 * kEp];
+    constexpr int kOffW = 2 * kX, kOffEp = 2 * kX + 2 * kW, kLds = kOffEp + 4 * kEp;
+    static_assert(NJ % kRing == 0 && kLateW < kEndX && kEndX <= kB1, "schedule");
+    static_assert(kLds <= 160 * 1024 / (NA == 4 ? 1 : 2), "LDS budget");
+    static_assert(kStores + kDmaX < 64 && kStores + kDmaW < 64, "vmcnt range");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    const int r = lane & 31, h = lane >> 5;
+    const int r = lane & 15, q = lane >> 4;
     const int wm = wave & 1, wn = wave >> 1;
     const int tiles_m = (M + TM - 1) / TM, tiles_n = (N + TN - 1) / TN;
     const int ntiles = tiles_m * tiles_n;
-    const int real = K / 64;                        // stages that hold channels of K
-    const int np = max((real + 1) / 2, 2);          // blocks of a tile
+    const int real = (K + 127) / 128;               // blocks that hold channels of K
+    const int np = ODD ? real : (real + 1) & ~1;    // blocks of a tile
     const int words = fp8_scale_words(K);
     const int nblocks = (N + kFp8Block - 1) / kFp8Block;
 
@@ -176,124 +200,176 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
         const uint32_t s = uint32_t(min(tm * TM + 64 * (wave % NA) + l, M - 1)) * 4u;
         return Aim{past ? kPast : x, past ? kPast : w, past ? kPast : s};
     };
-    // DMA instruction i of block p.  Where the block has only 64 channels, the upper
-    // chunks load the lower ones again; a block past the last loads the last again.
-    auto dma = [&](int slot, const Aim& t, int p, int i) {
+    // Where a block has only 64 channels, the upper chunks load the lower ones again;
+    // a block past the last loads the last again.
+    auto back_of = [&](int p) { return p * kRow + 64 < K || chunk < 4 ? 0u : 64u; };
+    auto dma_x = [&](int slot, uint32_t x, uint32_t s, int p, int i) {
         const uint32_t base = lds0 + uint32_t(slot);
-        const int pr = min(p, (real - 1) >> 1);
-        const uint32_t back = 2 * pr + 1 < real || chunk < 4 ? 0u : 64u;
-        if (i < kDmaX)
-            dma16(base + 1024 * (wave + 4 * i), t.x - back + uint32_t(32 * i) * uint32_t(K), rsX,
+        const int pr = min(p, real - 1);
+        if (i < kDmaX - 1)
+            dma16(base + 1024 * (wave + 4 * i), x - back_of(pr) + uint32_t(32 * i) * uint32_t(K), rsX,
                   uint32_t(pr * kRow));
-        else if (i < kDmaX + kDmaW)
-            dma16(base + kX + 1024 * (wave + 4 * (i - kDmaX)),
-                  t.w - back + uint32_t(32 * (i - kDmaX)) * uint32_t(K), rsW, uint32_t(pr * kRow));
         else
-            dma4(base + kX + kW + 256 * wave, t.s, rsS, uint32_t(pr >> 2) * uint32_t(M) * 4u);
+            dma4(base + TM * kRow + 256 * wave, s, rsS, uint32_t(pr >> 2) * uint32_t(M) * 4u);
+    };
+    auto dma_w = [&](int slot, uint32_t w, int p, int i) {
+        const int pr = min(p, real - 1);
+        dma16(lds0 + kOffW + uint32_t(slot) + 1024 * (wave + 4 * i),
+              w - back_of(pr) + uint32_t(32 * i) * uint32_t(K), rsW, uint32_t(pr * kRow));
     };
 
     // ---- fragments and instructions
     const int s128 = swz128(r);
-    const int offX = (wm * 32 * NA + r) * kRow, offW = kX + (wn * 32 * NB + r) * kRow;
-    const int offS = kX + kW + (wm * 32 * NA + r) * 4;
-    struct Frags {
-        i32x4 x[NA][2], w[NB][2];
+    const int offX = (wm * 32 * NA + r) * kRow, offS = TM * kRow + (wm * 32 * NA + r) * 4;
+    const int offW = kOffW + (wn * 32 * NB + r) * kRow;
+    struct Frag {
+        i32x4 lo, hi;
     };
-    Frags fr[2];
-    uint32_t sx[NA], sw[kBS];       // scale words of the block at hand
-    uint32_t sxn[NA], swn[kBS];     // and of the next
+    Frag x[2][NI], w[kRing];
+    uint32_t sx[NI], sw[kBS];       // scale words of the block at hand
+    uint32_t sxn[NI], swn[kBS];     // and of the next
     const uint32_t* wsp[kBS];       // the tile's scale words of W
-    auto read_n = [&](int slot, int half, Frags& f, int n) {
-        const int blk = n >> 1, part = n & 1;
-        const int c = 16 * ((4 * half + 2 * part + h) ^ s128);
-        if (blk < NA)
-            f.x[blk][part] = lds_read<i32x4>(smem + slot, offX + blk * 32 * kRow + c);
-        else
-            f.w[blk - NA][part] = lds_read<i32x4>(smem + slot, offW + (blk - NA) * 32 * kRow + c);
+    auto read = [&](int off, Frag& f, int part) {
+        (part ? f.hi : f.lo) = lds_read<i32x4>(smem, off + 16 * ((4 * part + q) ^ s128));
     };
-    auto read_scales = [&](int slot, uint32_t* s) {
-#pragma unroll
-        for (int a = 0; a < NA; ++a) s[a] = lds_read<uint32_t>(smem + slot, offS + a * 128);
-    };
-    f32x16 acc[NA][NB];
-    auto mma = [&](const Frags& f, int k, int shift, uint32_t keep, auto first) {
-        const int a = k % NA, b = k / NA;
-        const i32x8 vx = __builtin_shufflevector(f.x[a][0], f.x[a][1], 0, 1, 2, 3, 4, 5, 6, 7);
-        const i32x8 vw = __builtin_shufflevector(f.w[b][0], f.w[b][1], 0, 1, 2, 3, 4, 5, 6, 7);
-        acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            vw, vx, decltype(first)::value ? f32x16{} : acc[a][b], 0, 0, 0,
-            int((sw[kBS == 1 ? 0 : b] >> shift) & keep), 0, int((sx[a] >> shift) & keep));
-    };
-    int cur = 0;  // slot of the block at hand
-    // Stage `half` of block p on fragment set `half`: its instructions and the next
-    // stage's LDS reads.  A second half waits until at most `wait` later vector
-    // memory operations are under way, reads the next block's scale words and issues
-    // the first `loads` loads of block lp (aimed at `t`) into the slot it frees; a
-    // first half issues the others of the block that the stage before began.
-    auto stage = [&](auto half, auto first, auto wait, auto loads, int p, const Aim& t, int lp) {
-        constexpr int S = decltype(half)::value, kLoads = decltype(loads)::value;
-        constexpr int kB0 = S == 1 ? kBar + 1 : 0;        // the first read's place
-        constexpr int kReadIn = kM - kTail - kB0, kLoadIn = S == 1 ? kM - kB0 : kGaps0;
-        constexpr int kFrom = S == 1 ? 0 : kDma - kLoads;
-        const int nxt = S == 1 ? kSlot - cur : cur;       // where the reads go
+    f32x4 acc[NI][NJ];
+    int slot = 0;                   // 0 or 1: of the block at hand
+    int lpx = 0, lpw = 0;           // the blocks being loaded
+    uint32_t atx = 0, ats = 0, atw = 0;  // and their offsets
+    Aim next = {0, 0, 0};           // the next tile's
+    // Block p on fragment set S: waits for X (B0) and W (B1) until at most wait0 and
+    // wait1 later vector memory operations are under way; issues `late` loads of W that
+    // the block before left, X's loads, and `tail` loads of W.
+    auto block = [&](auto set, auto first, auto wait0, auto wait1, auto late, auto tail, int p) {
+        constexpr int S = decltype(set)::value;
+        constexpr int kLate = decltype(late)::value, kTail = decltype(tail)::value;
+        const int oth = 1 - slot;
         const int shift = 8 * (p & 3);                    // the block's byte in the scale words
-        const uint32_t keep = 2 * p + S < real ? 0xFFu : 0u;  // 2^-127 where filled up
-#pragma unroll
-        for (int k = 0; k < kM; ++k) {
-            mma(fr[S], k, shift, keep, first);
-            if (S == 0 && k == 0) {
-                // here, so that the scalar load has a stage's time before a wait counts it
-                const int w = min((p + 1) >> 2, words - 1);
-#pragma unroll
-                for (int b = 0; b < kBS; ++b) swn[b] = wsp[b][w];
-            }
-            if (S == 1 && k == kBar) {
-                wait_vmcnt_lgkm0<decltype(wait)::value>();
+        // 2^-127 for the channels it is filled up with
+        const uint32_t keep = p * kRow + 64 * (q >> 1) < K ? 0xFFu : 0u;
+        if (++lpx >= np) lpx = 0;
+        const bool over = lpx < 2;  // the next tile's
+        atx = over ? next.x : atx;
+        ats = over ? next.s : ats;
+        for_each([&](auto kc) {
+            constexpr int k = decltype(kc)::value, i = k % NI, j = k / NI;
+            const Frag &fx = x[S][i], &fw = w[j % kRing];
+            const i32x8 vx = __builtin_shufflevector(fx.lo, fx.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            const i32x8 vw = __builtin_shufflevector(fw.lo, fw.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                vw, vx, decltype(first)::value ? f32x4{} : acc[i][j], 0, 0, 0,
+                int((sw[kBS == 1 ? 0 : j / 2] >> shift) & keep), 0, int((sx[i] >> shift) & keep));
+            if constexpr (k == kB0) {
+                wait_vmcnt_lgkm0<decltype(wait0)::value>();
                 block_barrier();
-                read_scales(nxt, sxn);
             }
-            const int q = k - kB0;
-            if (q >= 0 && q < kLoadIn) {
+            if constexpr (k == kRead) {
+                // A scalar load under way turns every wait for LDS reads into a wait for all
+                // of them: it stands after the last read of X, half a dozen instructions
+                // before the next wait.
+                const int wd = min((p + 1) >> 2, words - 1);
 #pragma unroll
-                for (int i = q * kLoads / kLoadIn; i < (q + 1) * kLoads / kLoadIn; ++i)
-                    dma(S == 1 ? cur : kSlot - cur, t, lp, kFrom + i);
+                for (int b = 0; b < kBS; ++b) swn[b] = wsp[b][wd];
             }
-            if (q >= 0 && q < kReadIn) {
+            if constexpr (k == kB1) {
+                wait_vmcnt_lgkm0<decltype(wait1)::value>();
+                block_barrier();
+            }
+            // W's fragment j + 2, of the next block at the end
+            constexpr bool w_read = k % NI == 2 || k % NI == 3;
+            if constexpr (w_read) {
+                constexpr int n = (j + 2) % NJ;
+                const int sl = j + 2 < NJ ? slot : oth;
+                read(offW + sl * kW + n * 16 * kRow, w[(j + 2) % kRing], k % NI - 2);
+            }
+            // the other memory instructions stand where W is not read: X's fragments and
+            // scales (two rows' to an instruction) of the next block ...
+            if constexpr (!w_read && k > kB0 && k < kRead) {
+                constexpr int g = spare(NI, kB0 + 1, kRead), t = spare(NI, kB0 + 1, k), n = 5 * NI / 2;
+                for_each([&](auto mc) {
+                    constexpr int m = t * n / g + decltype(mc)::value;
+                    if constexpr (m % 5 < 4) {
+                        constexpr int f = m / 5 * 4 + m % 5;
+                        read(offX + oth * kX + (f / 2) * 16 * kRow, x[1 - S][f / 2], f % 2);
+                    } else {
+                        constexpr int f = m / 5;
+                        sxn[f] = lds_read<uint32_t>(smem, oth * kX + offS + f * 64);
+                        sxn[f + NI / 2] = lds_read<uint32_t>(smem, oth * kX + offS + (f + NI / 2) * 64);
+                    }
+                }, std::make_integer_sequence<int, (t + 1) * n / g - t * n / g>{});
+            }
+            // ... and the loads: the rest of W, X, the first of W after B1
+            if constexpr (!w_read && kLate > 0 && k < kLateW) {
+                constexpr int g = spare(NI, 0, kLateW), t = spare(NI, 0, k);
 #pragma unroll
-                for (int n = q * kReads / kReadIn; n < (q + 1) * kReads / kReadIn; ++n)
-                    read_n(nxt, 1 - S, fr[1 - S], n);
+                for (int n = t * kLate / g; n < (t + 1) * kLate / g; ++n)
+                    dma_w(oth * kW, atw, lpw, kDmaW - kLate + n);
+            }
+            if constexpr (!w_read && k >= kLateW && k < kEndX) {
+                constexpr int g = spare(NI, kLateW, kEndX), t = spare(NI, kLateW, k);
+#pragma unroll
+                for (int n = t * kDmaX / g; n < (t + 1) * kDmaX / g; ++n)
+                    dma_x(slot * kX, atx, ats, lpx, n);
+            }
+            if constexpr (k == kB1) {
+                lpw = lpx;
+                atw = over ? next.w : atw;
+            }
+            if constexpr (!w_read && kTail > 0 && k > kB1) {
+                constexpr int g = spare(NI, kB1 + 1, kM), t = spare(NI, kB1 + 1, k);
+#pragma unroll
+                for (int n = t * kTail / g; n < (t + 1) * kTail / g; ++n)
+                    dma_w(slot * kW, atw, lpw, n);
             }
             __builtin_amdgcn_sched_barrier(0);
-        }
-        if (S == 1) {
-            cur = nxt;
+        }, std::make_integer_sequence<int, kM>{});
+        slot = oth;
 #pragma unroll
-            for (int a = 0; a < NA; ++a) sx[a] = sxn[a];
+        for (int i = 0; i < NI; ++i) sx[i] = sxn[i];
 #pragma unroll
-            for (int b = 0; b < kBS; ++b) sw[b] = swn[b];
-        }
+        for (int b = 0; b < kBS; ++b) sw[b] = swn[b];
     };
 
     const __amdgpu_buffer_rsrc_t rsY =
         __builtin_amdgcn_make_buffer_rsrc(Y, 0, int(uint32_t(M) * uint32_t(N) * 2u), kRsrcWord3);
-    Aim at = aim(blockIdx.x);
+    {
+        const Aim at = aim(blockIdx.x);
+        atx = at.x;
+        ats = at.s;
+        atw = at.w;
+    }
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < 2; ++p) {
 #pragma unroll
-        for (int i = 0; i < kDma; ++i) dma(p * kSlot, at, p, i);
-    wait_vmcnt<0>();  // both: no stores stand between them and the first wait
+        for (int i = 0; i < kDmaX; ++i) dma_x(p * kX, atx, ats, p, i);
+#pragma unroll
+        for (int i = 0; i < kDmaW; ++i) dma_w(p * kW, atw, p, i);
+    }
+    wait_vmcnt<0>();  // both: no stores stand between them and the first waits (with ODD the
+                      // first block loads half of W's block 1 again)
     block_barrier();
-    read_scales(0, sx);
 #pragma unroll
-    for (int n = 0; n < kReads; ++n) read_n(0, 0, fr[0], n);
+    for (int n = 0; n < 2 * NI; ++n) read(offX + (n / 2) * 16 * kRow, x[0][n / 2], n % 2);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) read(offW + (n / 2) * 16 * kRow, w[n / 2], n % 2);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) sx[i] = lds_read<uint32_t>(smem, offS + i * 64);
 
-    using H0 = std::integral_constant<int, 0>;
-    using H1 = std::integral_constant<int, 1>;
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    using First = std::true_type;
+    using Other = std::false_type;
+    using AfterTail = std::integral_constant<int, kTailW>;      // of W, after X's last load
+    using AfterX = std::integral_constant<int, kDmaX>;          // of X, after W's last load
+    // a tile's first waits pass over the last one's stores: its first two blocks were
+    // loaded before them, W of block 1 wholly
+    using Stores0 = std::integral_constant<int, kDmaW + kStores>;
+    using Stores1 = std::integral_constant<int, kDmaX + kStores>;
+    using OddStores0 = std::integral_constant<int, kTailW + kStores>;
+    using Tail = std::integral_constant<int, kTailW>;
+    using Late = std::integral_constant<int, kDmaW - kTailW>;
+    using All = std::integral_constant<int, kDmaW>;
     using None = std::integral_constant<int, 0>;
-    using Some = std::integral_constant<int, kLoad1>;
-    using Rest = std::integral_constant<int, kDma - kLoad1>;
-    using All = std::integral_constant<int, kDma>;
-    using Stores = std::integral_constant<int, kStores>;
     for (int v = blockIdx.x; v < ntiles; v += gridDim.x) {
         int tm, tn;
         tile_of(v, tiles_m, tiles_n, tm, tn);
@@ -304,31 +380,35 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
                               min((col0 + 32 * b) / kFp8Block, nblocks - 1))) * size_t(words);
 #pragma unroll
         for (int b = 0; b < kBS; ++b) sw[b] = wsp[b][0];
-        const Aim next = aim(v + int(gridDim.x));
-        // block p's second stage loads block p + 2, or the next tile's p + 2 - np
-        int lp = 2;
-        auto cross = [&] {
-            if (lp >= np) lp -= np;
-            const bool over = lp < 2;
-            at = Aim{over ? next.x : at.x, over ? next.w : at.w, over ? next.s : at.s};
-        };
-        stage(H0{}, std::true_type{}, None{}, None{}, 0, at, 0);
-        cross();
-        // the first wait of a tile passes over the last one's stores: block 1 was
-        // loaded before them
-        stage(H1{}, std::false_type{}, Stores{}, Some{}, 0, at, lp);
-        for (int p = 1; p < np - 1; ++p) {
-            stage(H0{}, std::false_type{}, None{}, Rest{}, p, at, lp);
-            ++lp;
-            cross();
-            stage(H1{}, std::false_type{}, None{}, Some{}, p, at, lp);
+        next = aim(v + int(gridDim.x));
+        lpx = lpw = 1;  // block p loads block p + 2, or the next tile's p + 2 - np
+        if constexpr (ODD) {
+            // W of block 1 is half loaded after the last tile's stores, so that all pairs of
+            // blocks are alike and the registers suffice
+            block(S0{}, First{}, OddStores0{}, AfterX{}, Late{}, Tail{}, 0);
+            int p = 1;
+            do {
+                block(S1{}, Other{}, AfterTail{}, AfterX{}, Late{}, Tail{}, p);
+                block(S0{}, Other{}, AfterTail{}, AfterX{}, Late{}, Tail{}, p + 1);
+                p += 2;
+            } while (p < np);
+            // the next tile begins with set 0 again: its fragments now that it is free (their
+            // slot stays as it is until that tile's B1)
+#pragma unroll
+            for (int n = 0; n < 2 * NI; ++n)
+                read(offX + slot * kX + (n / 2) * 16 * kRow, x[0][n / 2], n % 2);
+        } else {
+            block(S0{}, First{}, Stores0{}, Stores1{}, None{}, Tail{}, 0);
+            for (int p = 1; p < np - 2; p += 2) {
+                block(S1{}, Other{}, AfterTail{}, AfterX{}, Late{}, Tail{}, p);
+                block(S0{}, Other{}, AfterTail{}, AfterX{}, Late{}, Tail{}, p + 1);
+            }
+            block(S1{}, Other{}, AfterTail{}, AfterX{}, Late{}, All{}, np - 1);
         }
-        stage(H0{}, std::false_type{}, None{}, Rest{}, np - 1, at, lp);
-        stage(H1{}, std::false_type{}, None{}, All{}, np - 1, at, 1);
         if constexpr (VEC)
-            store_block_rows(acc, rsY, N, row0, col0, smem + 2 * kSlot + wave * kEp);
+            store_block_rows<NA, NB>(acc, rsY, N, row0, col0, smem + kOffEp + wave * kEp);
         else
-            store_block_single(acc, rsY, N, row0, col0);
+            store_block_single<NA, NB>(acc, rsY, N, row0, col0);
     }
     wait_vmcnt<0>();  // the loads past the last tile still write LDS
 }
@@ -341,12 +421,18 @@ lynx_status launch_tiled(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq
     const long most = long(cus) * (NA == 4 ? 1 : 2);
     const dim3 grid(unsigned(tiles < most ? tiles : most));
     const uint32_t* ws = reinterpret_cast<const uint32_t*>(Ws);
-    if (N % 8 == 0)
-        hipLaunchKernelGGL((gemm_fp8_tiled<NA, NB, true>), grid, dim3(NT), 0, stream, Xq, Xs, Wq,
-                           ws, Y, M, N, K);
-    else
-        hipLaunchKernelGGL((gemm_fp8_tiled<NA, NB, false>), grid, dim3(NT), 0, stream, Xq, Xs, Wq,
-                           ws, Y, M, N, K);
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(NT), 0, stream, Xq, Xs, Wq, ws, Y, M, N, K);
+    };
+    constexpr bool kOdd = !(NA == 4 && NB == 4);
+    const bool odd = kOdd && K > 128 && (K + 127) / 128 % 2 != 0;
+    if (N % 8 == 0) {
+        if (odd) launch(gemm_fp8_tiled<NA, NB, true, kOdd>);
+        else launch(gemm_fp8_tiled<NA, NB, true, false>);
+    } else {
+        if (odd) launch(gemm_fp8_tiled<NA, NB, false, kOdd>);
+        else launch(gemm_fp8_tiled<NA, NB, false, false>);
+    }
     return launch_status();
 }
 
@@ -367,7 +453,9 @@ lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t*
     // 256 x 256 115; 9216 x 3072: 89 and 75; 512 x 3072: 128 x 128 14 us, 256 x 192 24.
     auto tiles = [&](int tm, int tn) { return long((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
     auto rounds = [](long t, long n) { return (t + n - 1) / n; };
-    const long wide = rounds(tiles(256, 256), cus) * 100, mid = rounds(tiles(256, 192), cus) * 83;
+    const long np = (K + 127) / 128;  // 256 x 256 tiles take an even number of K blocks
+    const long wide = rounds(tiles(256, 256), cus) * (100 * ((np + 1) & ~1L) / np);
+    const long mid = rounds(tiles(256, 192), cus) * 83;
     const long t22 = tiles(128, 128);
     const long small = t22 <= cus ? 45 : rounds(t22, 2 * cus) * 75;
     if (small < wide && small < mid)
