@@ -313,14 +313,16 @@ def _expect(t, dtype, shape, dev, name) -> int:
     return t.data_ptr()
 
 
-def _matrix(t, name):
-    """(rows, columns, device) of a 2-d device tensor."""
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix, got shape {tuple(t.shape)}")
-    dev = t.device
-    if dev.type != "cuda":
+def _rows(t, dtype, name):
+    """(rows, columns, device, data pointer) of a contiguous matrix on a device."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a matrix, got shape {tuple(shape)}")
+    if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
-    return t.shape[0], t.shape[1], dev
+    if t.dtype is not dtype or not t.is_contiguous():
+        _need(t, dtype, shape, name)
+    return shape[0], shape[1], t.device, t.data_ptr()
 
 
 _fns: dict = {}
@@ -355,13 +357,16 @@ def quantize_fp8(X: torch.Tensor, out: tuple | None = None):
     float8_e8m0fnu, the scale of row m and channels 128 kb .. 128 kb + 127 at
     scale[kb // 4, m, kb % 4].  out: the pair of tensors to write.
     """
-    M, K, dev = _matrix(X, "X")
-    x = _expect(X, torch.bfloat16, (M, K), dev, "X")
-    shape = (_scale_words(K), M, 4)
-    q, scale = out if out is not None else (torch.empty(M, K, dtype=FP8, device=dev),
-                                            torch.empty(shape, dtype=E8M0, device=dev))
-    _call("lynx_quantize_fp8", dev, x, M, K, _expect(q, FP8, (M, K), dev, "q"),
-          _expect(scale, E8M0, shape, dev, "scale"))
+    M, K, dev, x = _rows(X, torch.bfloat16, "X")
+    words = _scale_words(K)
+    if out is None:
+        q = torch.empty(M, K, dtype=FP8, device=dev)
+        scale = torch.empty(words, M, 4, dtype=E8M0, device=dev)
+    else:
+        q, scale = out
+        _expect(q, FP8, (M, K), dev, "q")
+        _expect(scale, E8M0, (words, M, 4), dev, "scale")
+    _call("lynx_quantize_fp8", dev, x, M, K, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -372,13 +377,16 @@ def quantize_fp8_weight(W: torch.Tensor, out: tuple | None = None):
     4 ceil(K/512)] float8_e8m0fnu, the scale of the block of 128 rows x 128
     channels (nb, kb) at scale[nb, kb].  out: the pair of tensors to write.
     """
-    N, K, dev = _matrix(W, "W")
-    w = _expect(W, torch.bfloat16, (N, K), dev, "W")
+    N, K, dev, w = _rows(W, torch.bfloat16, "W")
     shape = ((N + 127) // 128, 4 * _scale_words(K))
-    q, scale = out if out is not None else (torch.empty(N, K, dtype=FP8, device=dev),
-                                            torch.empty(shape, dtype=E8M0, device=dev))
-    _call("lynx_quantize_fp8_weight", dev, w, N, K, _expect(q, FP8, (N, K), dev, "q"),
-          _expect(scale, E8M0, shape, dev, "scale"))
+    if out is None:
+        q = torch.empty(N, K, dtype=FP8, device=dev)
+        scale = torch.empty(shape, dtype=E8M0, device=dev)
+    else:
+        q, scale = out
+        _expect(q, FP8, (N, K), dev, "q")
+        _expect(scale, E8M0, shape, dev, "scale")
+    _call("lynx_quantize_fp8_weight", dev, w, N, K, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -394,19 +402,19 @@ def _fp8_weight(Wq, Ws, K, dev):
 
 def linear_fp8(X, Wq, Ws, Y=None, workspace=None):
     """Y = Q(X) W^T with the weight (Wq, Ws) of quantize_fp8_weight (lynx_linear_fp8)."""
-    M, K, dev = _matrix(X, "X")
-    x = _expect(X, torch.bfloat16, (M, K), dev, "X")
+    M, K, dev, x = _rows(X, torch.bfloat16, "X")
     N, wq, ws = _fp8_weight(Wq, Ws, K, dev)
     if Y is None:
         Y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-    y = _expect(Y, torch.bfloat16, (M, N), dev, "Y")
+    else:
+        _expect(Y, torch.bfloat16, (M, N), dev, "Y")
     if workspace is None:
         nbytes = fp8_workspace_bytes(M, K)
         if nbytes > 0:
             workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: must be a contiguous tensor on {dev}")
-    _call("lynx_linear_fp8", dev, x, wq, ws, y, M, N, K, _ptr(workspace),
+    _call("lynx_linear_fp8", dev, x, wq, ws, Y.data_ptr(), M, N, K, _ptr(workspace),
           0 if workspace is None else workspace.numel() * workspace.element_size())
     return Y
 
@@ -414,14 +422,14 @@ def linear_fp8(X, Wq, Ws, Y=None, workspace=None):
 def linear_fp8_packed(q, scale, Wq, Ws, Y=None):
     """Y = X W^T of two 8-bit operands, (q, scale) of quantize_fp8 or a block norm
     and (Wq, Ws) of quantize_fp8_weight (lynx_linear_fp8_packed)."""
-    M, K, dev = _matrix(q, "q")
-    xq = _expect(q, FP8, (M, K), dev, "q")
+    M, K, dev, xq = _rows(q, FP8, "q")
     xs = _expect(scale, E8M0, (_scale_words(K), M, 4), dev, "scale")
     N, wq, ws = _fp8_weight(Wq, Ws, K, dev)
     if Y is None:
         Y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-    _call("lynx_linear_fp8_packed", dev, xq, xs, wq, ws,
-          _expect(Y, torch.bfloat16, (M, N), dev, "Y"), M, N, K)
+    else:
+        _expect(Y, torch.bfloat16, (M, N), dev, "Y")
+    _call("lynx_linear_fp8_packed", dev, xq, xs, wq, ws, Y.data_ptr(), M, N, K)
     return Y
 
 
@@ -443,14 +451,14 @@ def _sample_rows(t, C, dev, name):
 
 def _block_norm(x, y, gate, post_norm, post_weight, post_bias, post_eps, residual_scale, norm,
                 weight, bias, scale, shift, eps, fp8, x_out, out):
-    M, C, dev = _matrix(x, "x")
+    M, C, dev, xp = _rows(x, x.dtype, "x")
     f32 = x.dtype is torch.float32
     if not f32 and x.dtype is not torch.bfloat16:
         raise TypeError(f"x: expected torch.bfloat16 or torch.float32, got {x.dtype}")
     if norm not in NORM_KINDS or post_norm not in NORM_KINDS:
         raise ValueError(f"a norm is one of {list(NORM_KINDS)}")
     rows, bf16 = (M, C), torch.bfloat16
-    xp, yp, xo = _expect(x, x.dtype, rows, dev, "x"), None, None
+    yp = xo = None
     if y is not None:
         yp = _expect(y, bf16, rows, dev, "y")
         if x_out is None:
@@ -475,15 +483,20 @@ def _block_norm(x, y, gate, post_norm, post_weight, post_bias, post_eps, residua
         if fp8 or out is not None:
             raise ValueError("without a norm there is no second output")
     elif fp8:
-        shape = (_scale_words(C), M, 4)
+        words = _scale_words(C)
         if out is None:
             out = (torch.empty(M, C, dtype=FP8, device=dev),
-                   torch.empty(shape, dtype=E8M0, device=dev))
-        q, q_scale = _expect(out[0], FP8, rows, dev, "q"), _expect(out[1], E8M0, shape, dev, "q_scale")
+                   torch.empty(words, M, 4, dtype=E8M0, device=dev))
+        else:
+            _expect(out[0], FP8, rows, dev, "q")
+            _expect(out[1], E8M0, (words, M, 4), dev, "q_scale")
+        q, q_scale = out[0].data_ptr(), out[1].data_ptr()
     else:
         if out is None:
             out = torch.empty(M, C, dtype=bf16, device=dev)
-        h = _expect(out, bf16, rows, dev, "h")
+        else:
+            _expect(out, bf16, rows, dev, "h")
+        h = out.data_ptr()
     a = Norm(xp, yp, gp, channels(post_weight, "post_weight"), channels(post_bias, "post_bias"),
              channels(weight, "weight"), channels(bias, "bias"), sp, hp, xo, h, q, q_scale, M, C,
              samples, gs, ss, hs, residual_scale, post_eps, eps, f32, NORM_KINDS[post_norm],
