@@ -12,7 +12,7 @@
 // from the inputs (2^-4 of a value); the alternative that keeps every bit, the
 // bf16 instruction on widened values, runs at half the rate.
 //
-// A workgroup takes 16 CT columns; its WAVES waves take the K blocks in turn, straight
+// A workgroup takes 16 columns; its 8 waves take the K blocks in turn, straight
 // from global memory into registers: per 16 rows and block two loads of 16 bytes a
 // lane, each 64 contiguous bytes of 16 rows, the next block's before this block's
 // products.  The waves' sums are joined through LDS in wave order, so the result
@@ -20,7 +20,7 @@
 //
 // QUANT reads bf16 X and quantises it first, as lynx_quantize_fp8 does, into LDS: 16
 // lanes a row's block.  Every workgroup repeats that, so it is used where X is small
-// (kFewQuant elements); there it takes the place of a second kernel and of the
+// (fp8_few_quant); there it takes the place of a second kernel and of the
 // 8-bit copy in memory.
 #include "lynx_fp8.h"
 
@@ -31,56 +31,46 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8;
 
-template <int CT, bool QUANT>
+template <bool QUANT>
 __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
     const void* __restrict__ X, const uint32_t* __restrict__ Xs, const uint8_t* __restrict__ Wq,
     const uint32_t* __restrict__ Ws, uint16_t* __restrict__ Y, int M, int N, int K) {
-    __shared__ float part[kWaves][16][16 * CT + 1];
+    __shared__ float part[kWaves][16][17];
     // the rows' quantised blocks [block][row], 16-byte chunks swizzled by the row, and
     // their scales: at most M K + 64 M bytes, and a scale for each 128 of them
-    constexpr int kX = QUANT ? kFewQuant + 64 * kFewRows : 16;
+    constexpr int kX = QUANT ? kFewQuant + 64 * kFewQuantRows : 16;
     __shared__ __attribute__((aligned(16))) char xq[kX];
     __shared__ uint8_t xs[QUANT ? kX / kFp8Block : 16];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int r = lane & 15, q = lane >> 4;
-    const int n0 = int(blockIdx.x) * 16 * CT;
+    const int n0 = int(blockIdx.x) * 16;
     const int blocks = (K + kFp8Block - 1) / kFp8Block;
     const int words = fp8_scale_words(K);
 
     // rows past the end read the last row; their results are not stored
     const int xrow = min(r, M - 1);
     const uint8_t* a = static_cast<const uint8_t*>(X) + size_t(xrow) * size_t(K) + 16 * q;
-    const uint8_t* b[CT];
-    const uint32_t* bs[CT];
-#pragma unroll
-    for (int t = 0; t < CT; ++t) {
-        const int row = min(n0 + 16 * t + r, N - 1);
-        b[t] = Wq + size_t(row) * size_t(K) + 16 * q;
-        bs[t] = Ws + size_t(row / kFp8Block) * size_t(words);
-    }
+    const int wrow = min(n0 + r, N - 1);
+    const uint8_t* b = Wq + size_t(wrow) * size_t(K) + 16 * q;
+    const uint32_t* bs = Ws + size_t(wrow / kFp8Block) * size_t(words);
     struct Block {
-        i32x4 a[2], b[CT][2];
-        uint32_t sa, sb[CT];
+        i32x4 a[2], b[2];
+        uint32_t sa, sb;
     };
     auto load = [&](int kb, Block& o) {
         const int off = kb * kFp8Block;
         const bool upper = off + 64 < K;  // a last block of 64 channels has no upper half: zeros
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            o.b[t][0] = *reinterpret_cast<const i32x4*>(b[t] + off);
-            o.b[t][1] = upper ? *reinterpret_cast<const i32x4*>(b[t] + off + 64) : i32x4{};
-            o.sb[t] = bs[t][kb >> 2];
-        }
+        o.b[0] = *reinterpret_cast<const i32x4*>(b + off);
+        o.b[1] = upper ? *reinterpret_cast<const i32x4*>(b + off + 64) : i32x4{};
+        o.sb = bs[kb >> 2];
         if constexpr (!QUANT) {
             o.a[0] = *reinterpret_cast<const i32x4*>(a + off);
             o.a[1] = upper ? *reinterpret_cast<const i32x4*>(a + off + 64) : i32x4{};
             o.sa = Xs[size_t(kb >> 2) * size_t(M) + xrow];
         }
     };
-    f32x4 acc[CT];
-#pragma unroll
-    for (int j = 0; j < CT; ++j) acc[j] = f32x4{};
+    f32x4 acc = {};
     auto multiply = [&](int kb, const Block& o) {
         const int shift = 8 * (kb & 3);
         i32x4 lo = o.a[0], hi = o.a[1];
@@ -92,12 +82,9 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
             sa = xs[kb * M + xrow];
         }
         const i32x8 va = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-        for (int j = 0; j < CT; ++j) {
-            const i32x8 vb = __builtin_shufflevector(o.b[j][0], o.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, acc[j], 0, 0, 0, sa, 0,
-                                                                      int(o.sb[j] >> shift));
-        }
+        const i32x8 vb = __builtin_shufflevector(o.b[0], o.b[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, acc, 0, 0, 0, sa, 0,
+                                                               int(o.sb >> shift));
     };
     Block cur, next;
     int kb = wave;
@@ -126,12 +113,10 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
         cur = next;
     }
 #pragma unroll
-    for (int j = 0; j < CT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) part[wave][4 * q + e][16 * j + r] = acc[j][e];
+    for (int e = 0; e < 4; ++e) part[wave][4 * q + e][r] = acc[e];
     __syncthreads();
-    for (int o = threadIdx.x; o < 256 * CT; o += 64 * kWaves) {
-        const int row = o / (16 * CT), col = o % (16 * CT);
+    if (threadIdx.x < 256) {
+        const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) v += part[w][row][col];
@@ -141,32 +126,21 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
     }
 }
 
-template <int CT>
-lynx_status launch_few(const void* X, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws,
-                       uint16_t* Y, int M, int N, int K, hipStream_t stream) {
-    const dim3 grid(unsigned((N + 16 * CT - 1) / (16 * CT)));
-    const uint32_t *xs = reinterpret_cast<const uint32_t*>(Xs),
-                   *ws = reinterpret_cast<const uint32_t*>(Ws);
-    if (Xs)
-        hipLaunchKernelGGL((gemm_fp8_few<CT, false>), grid, dim3(64 * kWaves), 0, stream, X, xs, Wq,
-                           ws, Y, M, N, K);
-    else
-        hipLaunchKernelGGL((gemm_fp8_few<CT, true>), grid, dim3(64 * kWaves), 0, stream, X, xs, Wq,
-                           ws, Y, M, N, K);
-    return launch_status();
-}
-
 }  // namespace
 
 lynx_status launch_gemm_fp8_few(const void* X, const uint8_t* Xs, const uint8_t* Wq,
                                 const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
                                 hipStream_t stream) {
-    int cus = 0;
-    if (device_cu_count(&cus) != LYNX_OK) return LYNX_ERR_DEVICE;
-    // 32 columns a workgroup halve the reads of X where there are many rows and
-    // columns enough (16 x 3072 -> 18432: 15.0 us, 16 columns 16.1; 2 rows 12.3 and 11.5)
-    if (M > 8 && N >= 32 * cus) return launch_few<2>(X, Xs, Wq, Ws, Y, M, N, K, stream);
-    return launch_few<1>(X, Xs, Wq, Ws, Y, M, N, K, stream);
+    const dim3 grid(unsigned((N + 15) / 16));
+    const uint32_t *xs = reinterpret_cast<const uint32_t*>(Xs),
+                   *ws = reinterpret_cast<const uint32_t*>(Ws);
+    if (Xs)
+        hipLaunchKernelGGL(gemm_fp8_few<false>, grid, dim3(64 * kWaves), 0, stream, X, xs, Wq, ws, Y,
+                           M, N, K);
+    else
+        hipLaunchKernelGGL(gemm_fp8_few<true>, grid, dim3(64 * kWaves), 0, stream, X, xs, Wq, ws, Y,
+                           M, N, K);
+    return launch_status();
 }
 
 }  // namespace lynx

@@ -86,10 +86,14 @@ lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t*
                             hipStream_t stream);
 
 // Product kernels (launch_gemm_fp8 chooses).  _few: M <= kFewRows, from the 8-bit
-// operand, or from bf16 X quantised on the way in (Xs == nullptr).
+// operand, or (where fp8_few_quant) from bf16 X quantised on the way in (Xs ==
+// nullptr).
 constexpr int kFewRows = 16;
+constexpr int kFewQuantRows = 8;
 constexpr int kFewQuant = 32768;  // and at most so many elements of X
-inline bool fp8_few_quant(int64_t M, int64_t K) { return M <= kFewRows && M * K <= kFewQuant; }
+inline bool fp8_few_quant(int64_t M, int64_t K) {
+    return M <= kFewQuantRows && M * K <= kFewQuant;
+}
 lynx_status launch_gemm_fp8_few(const void* X, const uint8_t* Xs, const uint8_t* Wq,
                                 const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
                                 hipStream_t stream);

@@ -267,7 +267,7 @@ lynx_status lynx_quantize_fp8_weight(const uint16_t* W, int64_t N, int64_t K, ui
 /*
  * Bytes of device workspace lynx_linear_fp8 needs for an (M, K) activation: its
  * values and scales, each 256-byte aligned; 0 where it needs none (a few rows,
- * M <= 16 and M K <= 32768, are quantised inside the product) and for invalid sizes.
+ * M <= 8 and M K <= 32768, are quantised inside the product) and for invalid sizes.
  */
 size_t lynx_fp8_workspace_bytes(int64_t M, int64_t K);
 

@@ -27,9 +27,10 @@ def test_quantize_validation(fn, kw, status):
 
 def test_workspace_bytes():
     assert _abi.fp8_workspace_bytes(17, 128) == 2304 + 256
-    assert _abi.fp8_workspace_bytes(16, 2112) == 33792 + 512
+    assert _abi.fp8_workspace_bytes(9, 2048) == 18432 + 256
+    assert _abi.fp8_workspace_bytes(8, 4160) == 33280 + 512
     # few rows are quantised inside the product
-    assert _abi.fp8_workspace_bytes(16, 2048) == 0 and _abi.fp8_workspace_bytes(1, 12288) == 0
+    assert _abi.fp8_workspace_bytes(8, 4096) == 0 and _abi.fp8_workspace_bytes(1, 12288) == 0
     # 333 x 1472: values rounded up to 256, three scale words a row
     assert _abi.fp8_workspace_bytes(333, 1472) == 490240 + 4096
     assert _abi.fp8_workspace_bytes(333, 1472) >= 333 * 1472 + 3 * 333 * 4

@@ -256,7 +256,7 @@ def test_product_extreme_scales():
 
 # ---- the whole layer ---------------------------------------------------------------
 
-@pytest.mark.parametrize("M,K,N", [(1, 64, 40), (2, 3072, 1000), (15, 576, 130), (16, 2048, 9000), (1, 32768, 40),
+@pytest.mark.parametrize("M,K,N", [(1, 64, 40), (2, 3072, 1000), (15, 576, 130), (16, 2048, 9000), (1, 32768, 40), (8, 4096, 50), (8, 4160, 9000), (7, 64, 8200),
                                    (16, 2112, 8200), (3, 10880, 50), (16, 64, 33), (40, 1472, 70), (300, 640, 520),
                                    (1300, 448, 1100)])
 def test_layer_is_quantiser_then_product(M, K, N):
