@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Stores one wave's 32 NA x 32 NB output block straight from the accumulators,
+// Stores one wave's 128 x 32 NB output block straight from the accumulators,
 // for tiles whose columns all lie inside N (N % 8 == 0).  A lane holds one
 // column of each 32 x 32 tile, rows 8 (e / 4) + 4 h + e % 4.  Rows e and e + 1
 // (e even) are converted together; the pair is swapped with the neighbouring
@@ -66,8 +66,8 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // past M lie past the end of the buffer resource and are dropped.  The shape
 // limits keep (M + 256) N < 2^31, so the offsets of those rows cannot wrap.
 // row0, col0: the block's first output row and column.
-template <int NB, int NA>
-__device__ __forceinline__ void store_block_direct(const f32x16 (&acc)[NA][NB],
+template <int NB>
+__device__ __forceinline__ void store_block_direct(const f32x16 (&acc)[4][NB],
                                                    __amdgpu_buffer_rsrc_t rsY, int N, int row0,
                                                    int col0) {
     typedef float f32x2_t __attribute__((ext_vector_type(2)));
@@ -80,7 +80,7 @@ __device__ __forceinline__ void store_block_direct(const f32x16 (&acc)[NA][NB],
     const uint32_t vbase =
         (uint32_t(row0 + 4 * eh + (er & 1)) * uint32_t(N) + uint32_t(col0 + (er & ~1))) * 2u;
 #pragma unroll
-    for (int a = 0; a < NA; ++a)
+    for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
