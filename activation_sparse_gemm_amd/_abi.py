@@ -71,7 +71,7 @@ SIGNATURES = {
     "lynx_linear_sequence": (_I, [_LP, _I64, _P, _SZ, _P]),
     "lynx_quantize_fp8": (_I, [_P, _I64, _I64, _P, _P, _P]),
     "lynx_quantize_fp8_weight": (_I, [_P, _I64, _I64, _P, _P, _P]),
-    "lynx_fp8_workspace_bytes": (_SZ, [_I64, _I64]),
+    "lynx_fp8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "lynx_linear_fp8": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     "lynx_linear_fp8_packed": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     "lynx_block_norm": (_I, [_P, _P]),
@@ -396,8 +396,8 @@ def quantize_fp8_weight(W: torch.Tensor, out: tuple | None = None):
     return q, scale
 
 
-def fp8_workspace_bytes(M: int, K: int) -> int:
-    return lib().lynx_fp8_workspace_bytes(M, K)
+def fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return lib().lynx_fp8_workspace_bytes(M, N, K)
 
 
 def _fp8_weight(Wq, Ws, K, dev):
@@ -415,7 +415,7 @@ def linear_fp8(X, Wq, Ws, Y=None, workspace=None):
     else:
         _expect(Y, torch.bfloat16, (M, N), dev, "Y")
     if workspace is None:
-        nbytes = fp8_workspace_bytes(M, K)
+        nbytes = fp8_workspace_bytes(M, N, K)
         if nbytes > 0:
             workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():

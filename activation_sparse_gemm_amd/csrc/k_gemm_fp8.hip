@@ -441,13 +441,9 @@ lynx_status launch_tiled(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq
 lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                             const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
                             hipStream_t stream) {
+    if (fp8_is_few(M, N)) return launch_gemm_fp8_few(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
     int cus = 0;
     if (device_cu_count(&cus) != LYNX_OK) return LYNX_ERR_DEVICE;
-    // Few rows, unless there are enough columns to fill the chip with larger tiles, which
-    // read X less often: 16 x 3072 -> 3072 5.1 us, in 32 x 32 tiles 6.4; -> 9216 10.8, in 32 x
-    // 64 tiles 7.9; 4 rows -> 9216 8.4.
-    if (M <= kFewQuantRows || (M <= kFewRows && N < 32 * cus))
-        return launch_gemm_fp8_few(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
     bool taken = false;
     const lynx_status st = launch_gemm_fp8_mid(Xq, Xs, Wq, Ws, Y, M, N, K, cus, &taken, stream);
     if (taken) return st;
@@ -455,7 +451,7 @@ lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t*
     // 256 x 256 one (measured at K = 3072: 33 us; 256 x 192 0.83 of that; 128 x 128, two
     // workgroups a unit, 0.75, 0.45 with at most one).  4096 x 9216: 256 x 192 101 us,
     // 256 x 256 115; 9216 x 3072: 89 and 75; 512 x 3072: 128 x 128 14 us, 256 x 192 24.
-    auto tiles = [&](int tm, int tn) { return long((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+    auto tiles = [&](int tm, int tn) { return fp8_tiles(M, N, tm, tn); };
     auto rounds = [](long t, long n) { return (t + n - 1) / n; };
     const long np = (K + 127) / 128;  // 256 x 256 tiles take an even number of K blocks
     const long wide = rounds(tiles(256, 256), cus) * (100 * ((np + 1) & ~1L) / np);

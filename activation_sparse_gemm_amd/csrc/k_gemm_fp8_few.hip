@@ -20,7 +20,7 @@
 //
 // QUANT reads bf16 X and quantises it first, as lynx_quantize_fp8 does, into LDS: 16
 // lanes a row's block.  Every workgroup repeats that, so it is used where X is small
-// (fp8_few_quant); there it takes the place of a second kernel and of the
+// (fp8_fuse); there it takes the place of a second kernel and of the
 // 8-bit copy in memory.
 #include "lynx_fp8.h"
 
@@ -38,7 +38,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
     __shared__ float part[kWaves][16][17];
     // the rows' quantised blocks [block][row], 16-byte chunks swizzled by the row, and
     // their scales: at most M K + 64 M bytes, and a scale for each 128 of them
-    constexpr int kX = QUANT ? kFewQuant + 64 * kFewQuantRows : 16;
+    constexpr int kX = QUANT ? kFewQuant + 64 * kFewRows : 16;
     __shared__ __attribute__((aligned(16))) char xq[kX];
     __shared__ uint8_t xs[QUANT ? kX / kFp8Block : 16];
     const int lane = threadIdx.x & 63;

@@ -15,26 +15,35 @@
 // scale is not that of the lane's own channels but of a 32-channel piece of the
 // instruction's, so scales cannot mask half a block here.)  The groups' sums are
 // joined through LDS in order.
+//
+// QUANT reads bf16 X and quantises it on the way, as lynx_quantize_fp8 does: a step's
+// rows land as they are (256 bytes a block) and 16 lanes turn a row's block into its
+// values and scale, in LDS, before the fragments are read (a second barrier).  Every
+// column of tiles repeats that; it saves a kernel and the 8-bit copy's way through
+// memory.
 #include "lynx_fp8.h"
 #include "lynx_tile.h"
 
 namespace lynx {
 namespace {
 
-template <int RM, int CN, int KG, int SLOTS>
+template <int RM, int CN, int KG, int SLOTS, bool QUANT>
 __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
-    const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
+    const void* __restrict__ X, const uint8_t* __restrict__ Xs,
     const uint8_t* __restrict__ Wq, const uint32_t* __restrict__ Ws, uint16_t* __restrict__ Y,
     int M, int N, int K) {
     constexpr int TM = 32 * RM, TN = 32 * CN;       // waves 2 x 2 of 16 RM x 16 CN
-    constexpr int kX = TM * 128, kW = TN * 128;
-    constexpr int kGroup = kX + kW + 1024;          // one block: + a scale word per row of X
+    constexpr int kX = TM * (QUANT ? 256 : 128), kW = TN * 128;
+    constexpr int kGroup = kX + kW + (QUANT ? 0 : 1024);  // one block: + a scale word per row of X
     constexpr int kSlot = KG * kGroup;
-    constexpr int kDmaX = RM, kDmaW = CN, kDma = kDmaX + kDmaW + 1;  // per wave and step
+    // per wave and step
+    constexpr int kDmaX = QUANT ? 2 * RM : RM, kDmaW = CN, kDma = kDmaX + kDmaW + (QUANT ? 0 : 1);
     constexpr int kJoin = (KG - 1) * TM * TN * 4;
-    static_assert(TM <= 256 && SLOTS * kSlot <= 160 * 1024 && kJoin <= SLOTS * kSlot, "LDS budget");
+    constexpr int kQ = QUANT ? TM * 128 + TM : 0;         // a group's quantised block and scales
+    constexpr int kLds = SLOTS * kSlot + KG * kQ;
+    static_assert(TM <= 256 && kLds <= 160 * 1024 && kJoin <= SLOTS * kSlot, "LDS budget");
     static_assert((SLOTS - 2) * kDma < 64, "vmcnt range");
-    __shared__ __attribute__((aligned(1024))) char smem[SLOTS * kSlot];
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
 
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
@@ -50,14 +59,17 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
     const int nblocks = (N + kFp8Block - 1) / kFp8Block;
 
     const uint32_t lds0 = lds_addr(smem) + uint32_t(group * kGroup);
-    const i32x4 rsX = make_rsrc(Xq, uint32_t(M) * uint32_t(K));
+    const i32x4 rsX = make_rsrc(X, uint32_t(M) * uint32_t(K) * (QUANT ? 2u : 1u));
     const i32x4 rsW = make_rsrc(Wq, uint32_t(N) * uint32_t(K));
     const i32x4 rsS = make_rsrc(Xs, uint32_t(words) * uint32_t(M) * 4u);
     // DMA instruction j of wave w moves rows 8 w + l/8 + 32 j, lane l's 16 bytes the
     // chunk that the row's swizzle puts there (the same for every j)
     const int lrow = 8 * wave + (lane >> 3);
     const int chunk = (lane & 7) ^ swz128(lrow);
-    const uint32_t vx = uint32_t(tm * TM + lrow) * uint32_t(K) + uint32_t(16 * chunk);
+    // (QUANT: X's rows are 256 bytes, unswizzled: rows 4 w + l/16 + 16 j)
+    const int qrow = 4 * wave + (lane >> 4);
+    const uint32_t vx = QUANT ? uint32_t(tm * TM + qrow) * uint32_t(2 * K) + uint32_t(16 * r)
+                              : uint32_t(tm * TM + lrow) * uint32_t(K) + uint32_t(16 * chunk);
     const uint32_t vw = uint32_t(tn * TN + lrow) * uint32_t(K) + uint32_t(16 * chunk);
     // rows past the end take the last row's words (the word's offset is not range checked)
     const uint32_t vs = uint32_t(min(tm * TM + (64 * wave) % TM + lane, M - 1)) * 4u;
@@ -67,13 +79,21 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
         const uint32_t back = kb * kFp8Block + 64 < K || chunk < 4 ? 0u : 64u;
         const uint32_t off = uint32_t(kb) * kFp8Block;
 #pragma unroll
-        for (int j = 0; j < kDmaX; ++j)
-            dma16(base + 1024 * (wave + 4 * j), vx - back + uint32_t(32 * j) * uint32_t(K), rsX, off);
+        for (int j = 0; j < kDmaX; ++j) {
+            if constexpr (QUANT)
+                dma16(base + 1024 * (wave + 4 * j),
+                      vx - (kb * kFp8Block + 64 < K || r < 8 ? 0u : 128u) +
+                          uint32_t(16 * j) * uint32_t(2 * K), rsX, 2 * off);
+            else
+                dma16(base + 1024 * (wave + 4 * j), vx - back + uint32_t(32 * j) * uint32_t(K), rsX,
+                      off);
+        }
 #pragma unroll
         for (int j = 0; j < kDmaW; ++j)
             dma16(base + kX + 1024 * (wave + 4 * j), vw - back + uint32_t(32 * j) * uint32_t(K), rsW,
                   off);
-        dma4(base + kX + kW + 256 * wave, vs, rsS, uint32_t(kb >> 2) * uint32_t(M) * 4u);
+        if constexpr (!QUANT)
+            dma4(base + kX + kW + 256 * wave, vs, rsS, uint32_t(kb >> 2) * uint32_t(M) * 4u);
     };
 #pragma unroll
     for (int s = 0; s < SLOTS - 1; ++s) load(s, s);
@@ -83,7 +103,9 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
     const uint32_t* wsp = Ws + size_t(__builtin_amdgcn_readfirstlane(
                                    min(col0 / kFp8Block, nblocks - 1))) * size_t(words);
     const int sw = swz128(r);
-    const int offX = group * kGroup + (wm * 16 * RM + r) * 128;
+    char* const xq = smem + SLOTS * kSlot + group * kQ;      // QUANT: the group's values ...
+    uint8_t* const xs = reinterpret_cast<uint8_t*>(xq + TM * 128);  // ... and scales
+    const int offX = (QUANT ? 0 : group * kGroup) + (wm * 16 * RM + r) * 128;
     const int offW = group * kGroup + kX + (wn * 16 * CN + r) * 128;
     const int offS = group * kGroup + kX + kW + (wm * 16 * RM + r) * 4;
     f32x4 acc[RM][CN];
@@ -105,17 +127,37 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
         const bool upper = kb * kFp8Block + 64 < K;
         i32x8 x[RM], w[CN];
         uint32_t sx[RM];
-        auto frag = [&](int off, bool both) {
-            const i32x4 lo = lds_read<i32x4>(s, off + 16 * (q ^ sw));
-            const i32x4 hi = lds_read<i32x4>(s, off + 16 * ((4 + q) ^ sw));
+        auto frag = [&](const char* p, int off, bool both) {
+            const i32x4 lo = lds_read<i32x4>(p, off + 16 * (q ^ sw));
+            const i32x4 hi = lds_read<i32x4>(p, off + 16 * ((4 + q) ^ sw));
             return __builtin_shufflevector(lo, both ? hi : i32x4{}, 0, 1, 2, 3, 4, 5, 6, 7);
         };
 #pragma unroll
-        for (int i = 0; i < RM; ++i) x[i] = frag(offX + i * 16 * 128, true);
+        for (int j = 0; j < CN; ++j) w[j] = frag(s, offW + j * 16 * 128, upper);
+        if constexpr (QUANT) {
+            const bool in = kb * kFp8Block + 8 * r < K;  // channels past K count as zeros
 #pragma unroll
-        for (int j = 0; j < CN; ++j) w[j] = frag(offW + j * 16 * 128, upper);
+            for (int j = 0; j < kDmaX; ++j) {
+                const int row = qrow + 16 * j;
+                u32x4 v = lds_read<u32x4>(s, group * kGroup + row * 256 + 16 * r);
+                if (!in) v = u32x4{0, 0, 0, 0};
+                const uint32_t byte = fp8_scale_byte(row16_max(fp8_amax8(v)));
+                const float div = fp8_divisor(byte);
+                *reinterpret_cast<u32x2*>(xq + row * 128 + 16 * ((r >> 1) ^ swz128(row)) +
+                                          8 * (r & 1)) =
+                    u32x2{fp8_pack4(v[0], v[1], div), fp8_pack4(v[2], v[3], div)};
+                if (r == 0) xs[row] = uint8_t(byte);
+            }
+            wait_lgkm0();
+            block_barrier();
+        }
 #pragma unroll
-        for (int i = 0; i < RM; ++i) sx[i] = (lds_read<uint32_t>(s, offS + i * 64) >> shift) & keep;
+        for (int i = 0; i < RM; ++i) x[i] = frag(QUANT ? xq : s, offX + i * 16 * 128, true);
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+            if constexpr (QUANT) sx[i] = xs[wm * 16 * RM + 16 * i + r] & keep;
+            else sx[i] = (lds_read<uint32_t>(s, offS + i * 64) >> shift) & keep;
+        }
         const uint32_t sws = (ws >> shift) & keep;
 #pragma unroll
         for (int i = 0; i < RM; ++i)
@@ -172,16 +214,25 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
     }
 }
 
-template <int RM, int CN, int KG, int SLOTS>
-lynx_status launch_mid(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws,
+template <int RM, int CN, int KG, int SLOTS, bool QUANT = false>
+lynx_status launch_mid(const void* X, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws,
                        uint16_t* Y, int M, int N, int K, hipStream_t stream) {
-    const long tiles = long((M + 32 * RM - 1) / (32 * RM)) * ((N + 32 * CN - 1) / (32 * CN));
-    hipLaunchKernelGGL((gemm_fp8_mid<RM, CN, KG, SLOTS>), dim3(unsigned(tiles)), dim3(256 * KG), 0,
-                       stream, Xq, Xs, Wq, reinterpret_cast<const uint32_t*>(Ws), Y, M, N, K);
+    const int64_t tiles = fp8_tiles(M, N, 32 * RM, 32 * CN);
+    hipLaunchKernelGGL((gemm_fp8_mid<RM, CN, KG, SLOTS, QUANT>), dim3(unsigned(tiles)),
+                       dim3(256 * KG), 0, stream, X, Xs, Wq, reinterpret_cast<const uint32_t*>(Ws), Y, M, N, K);
     return launch_status();
 }
 
 }  // namespace
+
+lynx_status launch_gemm_fp8_mid_quant(const uint16_t* X, const uint8_t* Wq, const uint8_t* Ws,
+                                      uint16_t* Y, int M, int N, int K, Fp8Fuse how,
+                                      hipStream_t stream) {
+    // the tiles and groups of launch_gemm_fp8_mid, two slots of the larger steps
+    return how == Fp8Fuse::mid32
+               ? launch_mid<1, 1, 4, 2, true>(X, nullptr, Wq, Ws, Y, M, N, K, stream)
+               : launch_mid<1, 2, 2, 2, true>(X, nullptr, Wq, Ws, Y, M, N, K, stream);
+}
 
 lynx_status launch_gemm_fp8_mid(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                                 const uint8_t* Ws, uint16_t* Y, int M, int N, int K, int cus,
@@ -191,7 +242,7 @@ lynx_status launch_gemm_fp8_mid(const uint8_t* Xq, const uint8_t* Xs, const uint
     // K = 3072, us: 64 x 9216 32x32 11.6, 32x64 8.5; 128 x 3072 10.1 and 6.9; 4096 x 64
     // 5.8 and 6.7; 200 x 9216 32x128 14.3, 32x64 18.1; 512 x 3072 128x64 11.5, 32x128
     // 13.4, the tiled kernel's 128x128 14.1.
-    auto tiles = [&](int tm, int tn) { return long((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+    auto tiles = [&](int tm, int tn) { return fp8_tiles(M, N, tm, tn); };
     *taken = true;
     if (tiles(32, 32) <= cus) return launch_mid<1, 1, 4, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
     if (tiles(32, 64) <= 2 * cus) return launch_mid<1, 2, 2, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);

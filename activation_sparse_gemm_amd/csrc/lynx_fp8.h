@@ -85,18 +85,39 @@ lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t*
                             const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
                             hipStream_t stream);
 
-// Product kernels (launch_gemm_fp8 chooses).  _few: M <= kFewRows, from the 8-bit
-// operand, or (where fp8_few_quant) from bf16 X quantised on the way in (Xs ==
-// nullptr).
+// Product kernels (launch_gemm_fp8 chooses).  _few: M <= kFewRows; _mid: few output
+// tiles; each from the 8-bit operand, or from bf16 X quantised on the way in.
 constexpr int kFewRows = 16;
-constexpr int kFewQuantRows = 8;
-constexpr int kFewQuant = 32768;  // and at most so many elements of X
-inline bool fp8_few_quant(int64_t M, int64_t K) {
-    return M <= kFewQuantRows && M * K <= kFewQuant;
+constexpr int kFewQuant = 32768;  // elements of X that _few quantises
+
+// _few, unless there are enough columns to fill the chip with larger tiles, which read
+// X less often: 16 x 3072 -> 3072 5.1 us, in 32 x 32 tiles 6.4; -> 9216 10.8, in 32 x 64
+// tiles 7.9; 4 rows -> 9216 8.4.
+inline bool fp8_is_few(int64_t M, int64_t N) { return M <= 8 || (M <= kFewRows && N < 8192); }
+
+inline int64_t fp8_tiles(int64_t M, int64_t N, int64_t tm, int64_t tn) {
+    return (M + tm - 1) / tm * ((N + tn - 1) / tn);
 }
+
+// Whether lynx_linear_fp8 quantises inside the product, in the same tiles as the
+// product takes on a 256-unit device (so that its results are those of quantiser and
+// product).  It costs a product about 1.45 us per 1024 of K and saves a kernel (2.3 us
+// and its launch) and 3 bytes per element of X: worth it for short K or many rows.
+// 4096 x 3072 -> 64: 10.9 us, 15.0 apart; 300 x 1024 -> 1024: 5.8 and 6.7.
+enum class Fp8Fuse { no, few, mid32, mid64 };
+inline Fp8Fuse fp8_fuse(int64_t M, int64_t N, int64_t K) {
+    if (fp8_is_few(M, N)) return M * K <= kFewQuant ? Fp8Fuse::few : Fp8Fuse::no;
+    if (K > 2048 && M < 2048) return Fp8Fuse::no;
+    if (fp8_tiles(M, N, 32, 32) <= 256) return Fp8Fuse::mid32;
+    return fp8_tiles(M, N, 32, 64) <= 512 ? Fp8Fuse::mid64 : Fp8Fuse::no;
+}
+
 lynx_status launch_gemm_fp8_few(const void* X, const uint8_t* Xs, const uint8_t* Wq,
                                 const uint8_t* Ws, uint16_t* Y, int M, int N, int K,
                                 hipStream_t stream);
+lynx_status launch_gemm_fp8_mid_quant(const uint16_t* X, const uint8_t* Wq, const uint8_t* Ws,
+                                      uint16_t* Y, int M, int N, int K, Fp8Fuse how,
+                                      hipStream_t stream);
 // Takes the problem if its tile counts suit it; *taken says whether it did.
 lynx_status launch_gemm_fp8_mid(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                                 const uint8_t* Ws, uint16_t* Y, int M, int N, int K, int cus,

@@ -12,9 +12,9 @@ struct Fp8Layout {
     size_t q, scale, total;
 };
 
-Fp8Layout fp8_layout(int64_t M, int64_t K) {
+Fp8Layout fp8_layout(int64_t M, int64_t N, int64_t K) {
     Fp8Layout L = {0, 0, 0};
-    if (fp8_few_quant(M, K)) return L;  // quantised inside the product
+    if (fp8_fuse(M, N, K) != Fp8Fuse::no) return L;
     L.q = 0;
     L.scale = round_up256(size_t(M) * size_t(K));
     L.total = L.scale + round_up256(size_t(fp8_scale_words(int(K))) * size_t(M) * 4);
@@ -97,9 +97,9 @@ lynx_status lynx_quantize_fp8_weight(const uint16_t* W, int64_t N, int64_t K, ui
     return debug_sync(launch_quantize_fp8_weight(W, int(N), int(K), q, scale, s), s);
 }
 
-size_t lynx_fp8_workspace_bytes(int64_t M, int64_t K) {
-    if (!dims_ok(M, 1, K)) return 0;
-    return fp8_layout(M, K).total;
+size_t lynx_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (!dims_ok(M, N, K)) return 0;
+    return fp8_layout(M, N, K).total;
 }
 
 lynx_status lynx_linear_fp8(const uint16_t* X, const uint8_t* Wq, const uint8_t* Ws, uint16_t* Y,
@@ -109,7 +109,7 @@ lynx_status lynx_linear_fp8(const uint16_t* X, const uint8_t* Wq, const uint8_t*
     if (M == 0 || N == 0) return LYNX_OK;
     if (!X || !Wq || !Ws || !Y) return LYNX_ERR_NULL;
     if (!all16({X, Wq, Ws, Y})) return LYNX_ERR_ALIGN;
-    const Fp8Layout L = fp8_layout(M, K);
+    const Fp8Layout L = fp8_layout(M, N, K);
     if (L.total > 0) {
         if (!workspace || workspace_bytes < L.total) return LYNX_ERR_WORKSPACE;
         if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LYNX_ERR_ALIGN;
@@ -117,9 +117,12 @@ lynx_status lynx_linear_fp8(const uint16_t* X, const uint8_t* Wq, const uint8_t*
     lynx_status st = check_device();
     if (st != LYNX_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (L.total == 0)
+    const Fp8Fuse fuse = fp8_fuse(M, N, K);
+    if (fuse == Fp8Fuse::few)
+        return debug_sync(launch_gemm_fp8_few(X, nullptr, Wq, Ws, Y, int(M), int(N), int(K), s), s);
+    if (fuse != Fp8Fuse::no)
         return debug_sync(
-            launch_gemm_fp8_few(X, nullptr, Wq, Ws, Y, int(M), int(N), int(K), s), s);
+            launch_gemm_fp8_mid_quant(X, Wq, Ws, Y, int(M), int(N), int(K), fuse, s), s);
     uint8_t* q = static_cast<uint8_t*>(workspace) + L.q;
     uint8_t* scale = static_cast<uint8_t*>(workspace) + L.scale;
     st = launch_quantize_fp8(X, int(M), int(K), q, scale, s);

@@ -265,16 +265,17 @@ lynx_status lynx_quantize_fp8_weight(const uint16_t* W, int64_t N, int64_t K, ui
                                      uint8_t* scale, lynx_stream_t stream);
 
 /*
- * Bytes of device workspace lynx_linear_fp8 needs for an (M, K) activation: its
- * values and scales, each 256-byte aligned; 0 where it needs none (a few rows,
- * M <= 8 and M K <= 32768, are quantised inside the product) and for invalid sizes.
+ * Bytes of device workspace lynx_linear_fp8 needs for an (M, N, K) layer: the
+ * activation's values and scales, each 256-byte aligned; 0 where it needs none (few
+ * rows or few output tiles: X is quantised inside the product) and for invalid sizes.
  */
-size_t lynx_fp8_workspace_bytes(int64_t M, int64_t K);
+size_t lynx_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
- * The whole layer: quantises X into `workspace`, then the product.
+ * The whole layer: quantises X (into `workspace`, where it needs one), then the
+ * product; the same Y as lynx_quantize_fp8 and lynx_linear_fp8_packed.
  * Inputs: X [M][K] bf16; Wq, Ws a quantised weight [N][K].  Output: Y [M][N] bf16.
- * workspace: >= lynx_fp8_workspace_bytes(M, K) bytes, 256-byte aligned, contents
+ * workspace: >= lynx_fp8_workspace_bytes(M, N, K) bytes, 256-byte aligned, contents
  * on entry irrelevant, clobbered; NULL is allowed where that is 0.
  */
 lynx_status lynx_linear_fp8(const uint16_t* X, const uint8_t* Wq, const uint8_t* Ws, uint16_t* Y,

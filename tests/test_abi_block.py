@@ -26,24 +26,24 @@ def test_quantize_validation(fn, kw, status):
 
 
 def test_workspace_bytes():
-    assert _abi.fp8_workspace_bytes(17, 128) == 2304 + 256
-    assert _abi.fp8_workspace_bytes(9, 2048) == 18432 + 256
-    assert _abi.fp8_workspace_bytes(8, 4160) == 33280 + 512
-    # few rows are quantised inside the product
-    assert _abi.fp8_workspace_bytes(8, 4096) == 0 and _abi.fp8_workspace_bytes(1, 12288) == 0
-    # 333 x 1472: values rounded up to 256, three scale words a row
-    assert _abi.fp8_workspace_bytes(333, 1472) == 490240 + 4096
-    assert _abi.fp8_workspace_bytes(333, 1472) >= 333 * 1472 + 3 * 333 * 4
-    assert _abi.fp8_workspace_bytes(0, 64) == 0 and _abi.fp8_workspace_bytes(4, 100) == 0
-    assert _abi.fp8_workspace_bytes(-1, 64) == 0
+    ws = _abi.fp8_workspace_bytes
+    # values and scale words (one per row and 512 channels), each rounded up to 256
+    assert ws(4096, 12288, 3072) == 4096 * 3072 + 6 * 4096 * 4
+    assert ws(333, 4096, 1472) == 490240 + 4096
+    assert ws(9, 100, 4160) == 37632 + 512
+    # few rows and few tiles are quantised inside the product
+    assert ws(8, 100, 4096) == 0 and ws(1, 18432, 12288) == 0 and ws(16, 8191, 2048) == 0
+    assert ws(300, 1024, 1024) == 0 and ws(4096, 64, 3072) == 0 and ws(17, 16, 64) == 0
+    assert ws(8, 100, 4160) > 0 and ws(16, 8192, 2112) > 0 and ws(300, 1024, 2112) > 0
+    assert ws(0, 16, 64) == 0 and ws(4, 16, 100) == 0 and ws(-1, 16, 64) == 0
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(K=96), SHAPE), (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(M=1 << 20, N=1 << 12), SHAPE),
     (dict(x=None), NULL), (dict(wq=None), NULL), (dict(ws=None), NULL), (dict(y=None), NULL),
     (dict(x=A + 1), ALIGN), (dict(wq=A + 8), ALIGN), (dict(ws=A + 4), ALIGN), (dict(y=A + 2), ALIGN),
-    (dict(M=17, ws_=None), WORKSPACE), (dict(M=17, n=2304 + 255), WORKSPACE),
-    (dict(M=17, ws_=B + 16), ALIGN),
+    (dict(M=17, K=4096, ws_=None), WORKSPACE), (dict(M=17, K=4096, n=17 * 4096 + 767), WORKSPACE),
+    (dict(M=17, K=4096, ws_=B + 16), ALIGN),
     (dict(M=0), OK), (dict(N=0), OK),
 ])
 def test_linear_validation(kw, status):

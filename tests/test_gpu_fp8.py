@@ -258,6 +258,8 @@ def test_product_extreme_scales():
 # ---- the whole layer ---------------------------------------------------------------
 
 @pytest.mark.parametrize("M,K,N", [(1, 64, 40), (2, 3072, 1000), (15, 576, 130), (16, 2048, 9000), (1, 32768, 40), (8, 4096, 50), (8, 4160, 9000), (7, 64, 8200),
+                                   (16, 704, 8191), (33, 64, 40), (4100, 320, 64), (2049, 2240, 70), (500, 192, 2000),
+                                   (1000, 2048, 700), (40, 1984, 5000), (18, 448, 8192),
                                    (16, 2112, 8200), (3, 10880, 50), (16, 64, 33), (40, 1472, 70), (300, 640, 520),
                                    (1300, 448, 1100)])
 def test_layer_is_quantiser_then_product(M, K, N):
@@ -266,7 +268,7 @@ def test_layer_is_quantiser_then_product(M, K, N):
     X = dev(bits)
     say(f"linear_fp8 M={M} K={K} N={N}")
     Y = lynx.linear_fp8(X, wq, ws, Y=gu.nan_bf16((M, N)),
-                        workspace=gu.poisoned_bytes(lynx.fp8_workspace_bytes(M, K)))
+                        workspace=gu.poisoned_bytes(lynx.fp8_workspace_bytes(M, N, K)))
     check_product(Y, bo.values(*bo.quantize(x)), wv, f"layer {M}x{K}->{N}")
     Y2 = lynx.linear_fp8_packed(*lynx.quantize_fp8(X), wq, ws)
     assert torch.equal(Y.view(torch.int16), Y2.view(torch.int16))
@@ -303,7 +305,7 @@ def test_python_checks_name_the_argument():
         with pytest.raises(err, match=name):
             call()
     with pytest.raises(lynx.LynxError, match="LYNX_ERR_WORKSPACE"):
-        lynx.linear_fp8(dev(heavy(17, 128, 1)[0]), wq, ws, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        lynx.linear_fp8(dev(heavy(20, 4096, 1)[0]), *weight(24, 4096, 1)[:2], workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(lynx.LynxError, match="LYNX_ERR_SHAPE"):
         lynx.quantize_fp8(torch.zeros((2, 96), dtype=torch.bfloat16, device="cuda"))
 
@@ -324,7 +326,7 @@ def test_repeated_calls_two_streams_and_graph_replays_agree(M, K, N):
     torch.cuda.synchronize()
     assert all(torch.equal(Y.view(torch.int16), ref) for Y in outs)
     Y1, Y2 = gu.nan_bf16((M, N)), gu.nan_bf16((M, N))
-    ws1 = torch.empty(lynx.fp8_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    ws1 = torch.empty(lynx.fp8_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
     graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
     for g, Y in zip(graphs, (Y1, Y2)):        # two graphs that share a workspace
         with torch.cuda.graph(g):
