@@ -181,7 +181,7 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     const i32x4 rsX = make_rsrc(Xq, uint32_t(M) * uint32_t(K));
     const i32x4 rsW = make_rsrc(Wq, uint32_t(N) * uint32_t(K));
     const i32x4 rsS = make_rsrc(Xs, uint32_t(words) * uint32_t(M) * 4u);
-    const int chunk = (lane & 7) ^ swz128(8 * wave + (lane >> 3));
+    const int chunk = (lane & 7) ^ fp8_swz(8 * wave + (lane >> 3));
     struct Aim {
         uint32_t x, w, s;  // a tile's offsets, of instruction j = 0
     };
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     };
 
     // ---- fragments and instructions
-    const int s128 = swz128(r);
+    const int swz = fp8_swz(r);
     const int offX = (wm * 32 * NA + r) * kRow, offS = TM * kRow + (wm * 32 * NA + r) * 4;
     const int offW = kOffW + (wn * 32 * NB + r) * kRow;
     struct Frag {
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     uint32_t sxn[NI], swn[kBS];     // and of the next
     const uint32_t* wsp[kBS];       // the tile's scale words of W
     auto read = [&](int off, Frag& f, int part) {
-        (part ? f.hi : f.lo) = lds_read<i32x4>(smem, off + 16 * ((4 * part + q) ^ s128));
+        (part ? f.hi : f.lo) = lds_read<i32x4>(smem, off + 16 * ((4 * part + q) ^ swz));
     };
     f32x4 acc[NI][NJ];
     int slot = 0;                   // 0 or 1: of the block at hand

@@ -77,8 +77,8 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
         int sa = int(o.sa >> shift);
         if constexpr (QUANT) {
             const char* p = xq + (kb * M + xrow) * kFp8Block;
-            lo = *reinterpret_cast<const i32x4*>(p + 16 * (q ^ (xrow & 7)));
-            hi = *reinterpret_cast<const i32x4*>(p + 16 * ((4 + q) ^ (xrow & 7)));
+            lo = *reinterpret_cast<const i32x4*>(p + 16 * (q ^ fp8_swz(xrow)));
+            hi = *reinterpret_cast<const i32x4*>(p + 16 * ((4 + q) ^ fp8_swz(xrow)));
             sa = xs[kb * M + xrow];
         }
         const i32x8 va = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
                                                     size_t(row) * size_t(K) + c);
             const uint32_t byte = fp8_scale_byte(row16_max(fp8_amax8(v)));
             const float div = fp8_divisor(byte);
-            *reinterpret_cast<u32x2*>(xq + u * kFp8Block + 16 * ((l16 >> 1) ^ (row & 7)) +
+            *reinterpret_cast<u32x2*>(xq + u * kFp8Block + 16 * ((l16 >> 1) ^ fp8_swz(row)) +
                                       8 * (l16 & 1)) =
                 u32x2{fp8_pack4(v[0], v[1], div), fp8_pack4(v[2], v[3], div)};
             if (l16 == 0) xs[u] = uint8_t(byte);

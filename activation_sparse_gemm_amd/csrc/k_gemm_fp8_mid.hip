@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
     // DMA instruction j of wave w moves rows 8 w + l/8 + 32 j, lane l's 16 bytes the
     // chunk that the row's swizzle puts there (the same for every j)
     const int lrow = 8 * wave + (lane >> 3);
-    const int chunk = (lane & 7) ^ swz128(lrow);
+    const int chunk = (lane & 7) ^ fp8_swz(lrow);
     // (QUANT: X's rows are 256 bytes, unswizzled: rows 4 w + l/16 + 16 j)
     const int qrow = 4 * wave + (lane >> 4);
     const uint32_t vx = QUANT ? uint32_t(tm * TM + qrow) * uint32_t(2 * K) + uint32_t(16 * r)
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
     const int row0 = tm * TM + wm * 16 * RM, col0 = tn * TN + wn * 16 * CN;
     const uint32_t* wsp = Ws + size_t(__builtin_amdgcn_readfirstlane(
                                    min(col0 / kFp8Block, nblocks - 1))) * size_t(words);
-    const int sw = swz128(r);
+    const int sw = fp8_swz(r);
     char* const xq = smem + SLOTS * kSlot + group * kQ;      // QUANT: the group's values ...
     uint8_t* const xs = reinterpret_cast<uint8_t*>(xq + TM * 128);  // ... and scales
     const int offX = (QUANT ? 0 : group * kGroup) + (wm * 16 * RM + r) * 128;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
                 if (!in) v = u32x4{0, 0, 0, 0};
                 const uint32_t byte = fp8_scale_byte(row16_max(fp8_amax8(v)));
                 const float div = fp8_divisor(byte);
-                *reinterpret_cast<u32x2*>(xq + row * 128 + 16 * ((r >> 1) ^ swz128(row)) +
+                *reinterpret_cast<u32x2*>(xq + row * 128 + 16 * ((r >> 1) ^ fp8_swz(row)) +
                                           8 * (r & 1)) =
                     u32x2{fp8_pack4(v[0], v[1], div), fp8_pack4(v[2], v[3], div)};
                 if (r == 0) xs[row] = uint8_t(byte);

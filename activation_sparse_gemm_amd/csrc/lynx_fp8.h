@@ -15,6 +15,13 @@ constexpr uint32_t kScaleNaN = 255;   // E8M0 byte of NaN
 // Scale words of a row: four K blocks to a 32-bit word.
 inline __host__ __device__ int fp8_scale_words(int K) { return (K + 511) / 512; }
 
+// 16-byte chunk swizzle of 128-byte LDS rows that 16 x 16 x 128 fragments are read from
+// (lane l: row l % 16, chunk l / 16 or 4 + l / 16).  A 16-byte read is served in groups
+// of 16 lanes that hold rows 0-3 and 12-15 of one chunk and 4-11 of the next (or the
+// other way round), not in order: rows of a parity (half the banks each) then fall on
+// eight unlike chunks.  A row & 7 swizzle had 2-way conflicts on every read.
+__device__ __forceinline__ int fp8_swz(int row) { return (row >> 1) & 7; }
+
 // max over the 16 lanes of a DPP row, in every lane of the row
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
     v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x128, 0xF, 0xF, false)));
