@@ -450,7 +450,7 @@ lynx_status launch_gemm_fp8(const uint8_t* Xq, const uint8_t* Xs, const uint8_t*
     // Rounds of tiles over the compute units, each at its tile's time relative to a
     // 256 x 256 one (measured at K = 3072: 33 us; 256 x 192 0.83 of that; 128 x 128, two
     // workgroups a unit, 0.75, 0.45 with at most one).  4096 x 9216: 256 x 192 101 us,
-    // 256 x 256 115; 9216 x 3072: 89 and 75; 512 x 3072: 128 x 128 14 us, 256 x 192 24.
+    // 256 x 256 115; 9216 x 3072: 89 and 75; 512 x 12288: 128 x 128 25, 256 x 192 28.
     auto tiles = [&](int tm, int tn) { return fp8_tiles(M, N, tm, tn); };
     auto rounds = [](long t, long n) { return (t + n - 1) / n; };
     const long np = (K + 127) / 128;  // 256 x 256 tiles take an even number of K blocks

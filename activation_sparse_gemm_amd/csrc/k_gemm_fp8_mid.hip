@@ -237,17 +237,31 @@ lynx_status launch_gemm_fp8_mid_quant(const uint16_t* X, const uint8_t* Wq, cons
 lynx_status launch_gemm_fp8_mid(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                                 const uint8_t* Ws, uint16_t* Y, int M, int N, int K, int cus,
                                 bool* taken, hipStream_t stream) {
-    // The largest tile that still gives most compute units one (two where two
-    // workgroups fit a unit); small tiles split K over more groups instead.  At
-    // K = 3072, us: 64 x 9216 32x32 11.6, 32x64 8.5; 128 x 3072 10.1 and 6.9; 4096 x 64
-    // 5.8 and 6.7; 200 x 9216 32x128 14.3, 32x64 18.1; 512 x 3072 128x64 11.5, 32x128
-    // 13.4, the tiled kernel's 128x128 14.1.
+    // The smallest tile of which a compute unit gets no more than one: a second round costs
+    // a whole tile's time, and a larger tile leaves units idle.  K = 3072, us: 200 x 3072
+    // 64x64 8.4, 32x64 10.6, 96x64 9.8; 333 x 3072 96x64 9.9, 128x64 11.7; 160 x 9216
+    // 64x128 12.3, 64x64 15.9, 96x128 14.7; 200 x 9216 96x128 14.9, 128x128 17.2.
+    // 128x128 tiles pay against the tiled kernel's where K is long (1024 x 3072 18.0 and
+    // 19.7, but K = 1024, N = 4096 9.7 and 8.7), four groups instead of two too (160 x
+    // 12288 -> 3072 18.1 and 21.2; K = 1472, N = 1102 5.5 and 5.3; where many rows are
+    // quantised inside the product that has two).  Past that the tiled kernel, but for
+    // few rows (32 x 73728 32x64 34.8, tiled 45.9; 64 x 73728 64x128 42.4, 46.3) and
+    // where only two 64x128 tiles a unit come out even (192 x 18432 20.5, 23.7).
     auto tiles = [&](int tm, int tn) { return fp8_tiles(M, N, tm, tn); };
+    auto go = [&](auto kernel) { return kernel(Xq, Xs, Wq, Ws, Y, M, N, K, stream); };
     *taken = true;
-    if (tiles(32, 32) <= cus) return launch_mid<1, 1, 4, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
-    if (tiles(32, 64) <= 2 * cus) return launch_mid<1, 2, 2, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
-    if (tiles(128, 64) <= cus) return launch_mid<4, 2, 2, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
-    if (tiles(32, 128) <= 2 * cus) return launch_mid<1, 4, 1, 3>(Xq, Xs, Wq, Ws, Y, M, N, K, stream);
+    if (tiles(32, 32) <= cus) return go(launch_mid<1, 1, 4, 3>);
+    if (tiles(32, 64) <= cus)
+        return K >= 4096 && M < 2048 ? go(launch_mid<1, 2, 4, 3>) : go(launch_mid<1, 2, 2, 3>);
+    if (tiles(64, 64) <= cus) return go(launch_mid<2, 2, 2, 3>);
+    if (tiles(96, 64) <= cus) return go(launch_mid<3, 2, 2, 3>);
+    if (tiles(128, 64) <= cus) return go(launch_mid<4, 2, 2, 3>);
+    if (tiles(64, 128) <= cus) return go(launch_mid<2, 4, 2, 3>);
+    if (tiles(96, 128) <= cus) return go(launch_mid<3, 4, 2, 2>);
+    if (tiles(128, 128) <= cus && K > 2048) return go(launch_mid<4, 4, 2, 2>);
+    if (M <= 32) return go(launch_mid<1, 2, 2, 3>);
+    if (M <= 64 || (tiles(128, 128) > cus && tiles(64, 128) <= 2 * cus))
+        return go(launch_mid<2, 4, 1, 3>);
     *taken = false;
     return LYNX_OK;
 }

@@ -273,7 +273,9 @@ size_t lynx_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
  * The whole layer: quantises X (into `workspace`, where it needs one), then the
- * product; the same Y as lynx_quantize_fp8 and lynx_linear_fp8_packed.
+ * product; on a device of 256 compute units the same Y, bit for bit, as
+ * lynx_quantize_fp8 and lynx_linear_fp8_packed (on another, sums may be ordered
+ * otherwise).
  * Inputs: X [M][K] bf16; Wq, Ws a quantised weight [N][K].  Output: Y [M][N] bf16.
  * workspace: >= lynx_fp8_workspace_bytes(M, N, K) bytes, 256-byte aligned, contents
  * on entry irrelevant, clobbered; NULL is allowed where that is 0.

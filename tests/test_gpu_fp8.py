@@ -169,14 +169,19 @@ def test_non_finite_values_reach_their_row_only(M, N):
 
 # ---- the product -------------------------------------------------------------------
 
-# every kernel: M <= 16; 32x32, 32x64, 128x64 and 32x128 tiles of a split K; 128x128,
+# every kernel: M <= 16; tiles from 32x32 to 128x128 of a split K; persistent 128x128,
 # 256x192 and 256x256 tiles; each with ragged rows and columns, N % 8, N % 4, N % 2 == 0 and
 # odd N, K % 128 == 64 and K below the ring depth (unlike block scales show a wrong one)
 SHAPES = [(9, 3072, 8200), (16, 64, 9001), (190, 704, 9100), (190, 64, 9101), (500, 832, 2050), (1, 64, 1), (1, 128, 32), (2, 3072, 640), (16, 192, 17), (17, 320, 33), (31, 576, 130),
           (32, 12288, 64), (33, 64, 65), (64, 448, 200), (65, 1024, 127), (77, 3072, 384), (100, 640, 130),
           (255, 960, 257), (300, 1152, 1000), (1000, 1472, 1102), (4096, 256, 64), (64, 256, 4100),
           (1024, 64, 1024), (1030, 128, 1100), (1500, 704, 1288), (2048, 192, 1536), (700, 2112, 3000),
-          (3000, 64, 1700), (1700, 320, 1291)]
+          (3000, 64, 1700), (1700, 320, 1291),
+          # the tile sizes in turn: 32x64 in four groups, 64x64, 96x64, 128x64, 64x128, 96x128,
+          # 128x128, then few rows and many columns, and 64x128 two to a unit
+          (100, 4160, 3000), (200, 320, 3003), (333, 576, 3004), (333, 64, 3000), (500, 448, 3000),
+          (150, 320, 9101), (200, 704, 9101), (190, 64, 9104), (300, 2112, 9100), (350, 2176, 9001),
+          (20, 192, 40001), (50, 192, 40002), (160, 192, 18433), (160, 64, 18440)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
