@@ -61,27 +61,39 @@ __device__ __forceinline__ void store_f32(float* p, const Vec8& v) {
     *reinterpret_cast<f32x4*>(p + 4) = f32x4{v.f[4], v.f[5], v.f[6], v.f[7]};
 }
 
-// sum over the row's W waves, in every lane; `slot`: W floats of LDS that no
-// earlier sum since the row before last used
+// v plus its copies 8, 4, 2 and 1 lanes round the 16-lane row, from the step `from` on:
+// every lane adds the same pairs, so all of them get the same bits
+template <int FROM>
+__device__ __forceinline__ float row16_sum(float v) {
+#define LYNX_ROR(n) \
+    if constexpr (n <= FROM) \
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + n, 0xF, 0xF, false))
+    LYNX_ROR(8);
+    LYNX_ROR(4);
+    LYNX_ROR(2);
+    LYNX_ROR(1);
+#undef LYNX_ROR
+    return v;
+}
+
+// sum over the row's W waves, in every lane; `slot`: 4 W floats of LDS that no
+// earlier sum since the row before last used.  The waves' 16-lane sums are joined by
+// every lane from its share of them: fewer instructions than adding them all up.
 template <int W>
 __device__ __forceinline__ float row_sum(float v, float* slot) {
-#define LYNX_ROR(ctrl) \
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xF, 0xF, false))
-    LYNX_ROR(0x128);
-    LYNX_ROR(0x124);
-    LYNX_ROR(0x122);
-    LYNX_ROR(0x121);
-#undef LYNX_ROR
-    auto lane = [&](int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); };
-    float s = (lane(0) + lane(16)) + (lane(32) + lane(48));
-    if constexpr (W > 1) {
-        if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = s;
+    v = row16_sum<8>(v);
+    if constexpr (W == 1) {
+        auto lane = [&](int l) {
+            return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+        };
+        return (lane(0) + lane(16)) + (lane(32) + lane(48));
+    } else {
+        const int t = threadIdx.x;
+        if ((t & 15) == 0) slot[t >> 4] = v;
         __syncthreads();
-        s = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) s += slot[w];
+        if constexpr (W == 8) return row16_sum<8>(slot[t & 15] + slot[16 + (t & 15)]);
+        else return row16_sum<2 * W>(slot[t & (4 * W - 1)]);
     }
-    return s;
 }
 
 // v becomes v - mean (layer norm); returns 1 / sqrt(mean square + eps)
@@ -98,19 +110,20 @@ __device__ __forceinline__ float normalise(Vec8 (&v)[NV], const bool (&in)[NV], 
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i].f[j] = in[i] ? v[i].f[j] - mean : 0.f;
+            for (int j = 0; j < 8; ++j)
+                if (in[i]) v[i].f[j] -= mean;  // the others stay 0
     }
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) s = fmaf(v[i].f[j], v[i].f[j], s);
-    return rsqrtf(fmaf(row_sum<W>(s, slots + W), inv_c, eps));
+    return rsqrtf(fmaf(row_sum<W>(s, slots + 4 * W), inv_c, eps));
 }
 
 template <int W, int NV, bool XF32, bool HASY>
 __global__ __launch_bounds__(64 * W) void block_norm_kernel(const NormArgs A) {
-    __shared__ float slots[2][4 * W];
+    __shared__ float slots[2][16 * W];
     const int lane = threadIdx.x & 63;
     const int wave = W > 1 ? __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)) : 0;
     const int begin = int(blockIdx.x) * A.rows_per_group, end = min(begin + A.rows_per_group, A.M);
@@ -229,7 +242,7 @@ __global__ __launch_bounds__(64 * W) void block_norm_kernel(const NormArgs A) {
             for (int i = 0; i < NV; ++i) v[i] = x_of(i);
         }
         if (A.norm) {
-            const float rs = normalise<W>(v, in, A.norm, A.inv_c, A.eps, sl + 2 * W);
+            const float rs = normalise<W>(v, in, A.norm, A.inv_c, A.eps, sl + 8 * W);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (in[i]) {
@@ -240,11 +253,11 @@ __global__ __launch_bounds__(64 * W) void block_norm_kernel(const NormArgs A) {
                     if (A.h) store_bf16(A.h + base + c[i], v[i]);
                 }
                 if (A.q) {  // every lane: the group's maximum crosses lanes
-                    uint32_t m = 0;
+                    float m = 0.f;  // keeps a NaN; lanes past C hold zeros
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        m = max(m, in[i] ? __float_as_uint(v[i].f[j]) & 0x7FFFFFFFu : 0u);
-                    const uint32_t byte = fp8_scale_byte(row16_max(m));
+                        m = __builtin_elementwise_maximum(m, fabsf(v[i].f[j]));
+                    const uint32_t byte = fp8_scale_byte(row16_max(__float_as_uint(m)));
                     const float div = fp8_divisor(byte);
                     const float* f = v[i].f;
                     if (in[i])
@@ -311,8 +324,9 @@ lynx_status launch_block_norm(const lynx_norm& d, hipStream_t stream) {
     a.norm = d.norm;
     const bool f32 = d.x_fp32 != 0;
     // As many waves as give each lane 8 channels, up to 8 waves, a power of two: few
-    // registers, so many waves to a SIMD.  9216 x 3072 with y and 8-bit output: 8 waves
-    // 44 us (4.5 TB/s), 6 waves 48, 3 waves of 16 channels a lane 47, 2 of 24 48-49.
+    // registers, so many waves to a SIMD.  9216 x 3072 with y and 8-bit output, from HBM:
+    // 8 waves 43 us (4.6 TB/s), 4 waves of 16 channels a lane 47, 2 of 24 48; 4096 x 3072
+    // with fp32 x and bf16 output 33, 34 and 44.
     const int v = int((d.C + 511) / 512);  // 8-channel vectors of a wave, over the row
     if (v <= 1) launch<1, 1>(a, f32, cus, stream);
     else if (v <= 2) launch<2, 1>(a, f32, cus, stream);
