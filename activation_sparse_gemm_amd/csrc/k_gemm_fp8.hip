@@ -154,6 +154,10 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     constexpr int kStores = 2 * NA * NB;            // stores of an epilogue, at least
     constexpr int kEp = 64 * epilogue_columns(NA, NB);  // a wave's LDS for the epilogue
     constexpr int kBS = NB == 3 ? NB : 1;           // scale blocks a wave's columns touch
+    // rows of tiles that an XCD walks down together.  16384 x 4096 -> 4096 6 rows 201 us, 4
+    // 208, 8 217; 9216 x 3072 -> 12288 270, 266, 274; 256 x 192 tiles, 6000 x 4096 -> 11008
+    // 234, 221, 228.  Eight rows of 128 for the small tiles, two workgroups a unit.
+    constexpr int kGroup = NA == 2 ? 8 : NB == 3 ? 4 : 6;
     // past the end of X and W (they hold less than 2^31 bytes, and a tile's rows
     // span less than 2^31: kPast plus a row's offset does not wrap)
     constexpr uint32_t kPast = 0x80000000u;
@@ -189,7 +193,7 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     // from past the ends of the buffers: they read nothing.
     auto aim = [&](int v) {
         int tm, tn;
-        tile_of(min(v, ntiles - 1), tiles_m, tiles_n, tm, tn);
+        tile_of(min(v, ntiles - 1), tiles_m, tiles_n, tm, tn, kGroup);
         const bool past = v >= ntiles;
         const int l = fresh_lane();
         const uint32_t row = uint32_t(8 * wave + (l >> 3)), c = uint32_t(16 * chunk);
@@ -372,7 +376,7 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     using None = std::integral_constant<int, 0>;
     for (int v = blockIdx.x; v < ntiles; v += gridDim.x) {
         int tm, tn;
-        tile_of(v, tiles_m, tiles_n, tm, tn);
+        tile_of(v, tiles_m, tiles_n, tm, tn, kGroup);
         const int row0 = tm * TM + wm * 32 * NA, col0 = tn * TN + wn * 32 * NB;
 #pragma unroll
         for (int b = 0; b < kBS; ++b)

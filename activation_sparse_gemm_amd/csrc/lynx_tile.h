@@ -13,15 +13,16 @@ constexpr int BM = 256, NT = 256, GROUP_M = 8;
 __device__ __forceinline__ int swz64(int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }
 __device__ __forceinline__ int swz128(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-__device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int& tm, int& tn) {
+__device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int& tm, int& tn,
+                                        int group_m = GROUP_M) {
     const int ntiles = tiles_m * tiles_n;
     const int xcd = bid & 7, slot = bid >> 3;
     const int per = ntiles >> 3, rem = ntiles & 7;
     const int v = xcd * per + min(xcd, rem) + slot;
-    const int group_size = GROUP_M * tiles_n;
+    const int group_size = group_m * tiles_n;
     const int group = v / group_size;
-    const int first_m = group * GROUP_M;
-    const int gm = min(tiles_m - first_m, GROUP_M);
+    const int first_m = group * group_m;
+    const int gm = min(tiles_m - first_m, group_m);
     const int in = v - group * group_size;
     tm = first_m + in % gm;
     tn = in / gm;
