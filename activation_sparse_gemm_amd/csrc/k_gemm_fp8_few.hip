@@ -14,8 +14,9 @@
 //
 // A workgroup takes 16 columns; its 8 waves take the K blocks in turn, straight
 // from global memory into registers: per 16 rows and block two loads of 16 bytes a
-// lane, each 64 contiguous bytes of 16 rows, the next block's before this block's
-// products.  The waves' sums are joined through LDS in wave order, so the result
+// lane, each 64 contiguous bytes of 16 rows, three blocks under way (from HBM: 2 x 3072
+// -> 18432 12.8 us = 4.4 TB/s, two blocks 14.4; 1 x 12288 -> 3072 11.5 and 14.1; 16 waves
+// 13.8 and 11.5; from the cache 11.2 and 12.3).  The waves' sums are joined through LDS in wave order, so the result
 // does not depend on timing.
 //
 // QUANT reads bf16 X and quantises it first, as lynx_quantize_fp8 does, into LDS: 16
@@ -30,6 +31,7 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8;
+constexpr int kDepth = 3;  // blocks of a wave that are under way
 
 template <bool QUANT>
 __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
@@ -86,9 +88,10 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
         acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, acc, 0, 0, 0, sa, 0,
                                                                int(o.sb >> shift));
     };
-    Block cur, next;
-    int kb = wave;
-    if (kb < blocks) load(kb, cur);
+    Block ring[kDepth];
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i)
+        if (wave + i * kWaves < blocks) load(wave + i * kWaves, ring[i]);
     if constexpr (QUANT) {
         const int l16 = lane & 15;
         for (int u = wave * 4 + q; u < M * blocks; u += 4 * kWaves) {
@@ -107,10 +110,14 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_few(
         }
         __syncthreads();
     }
-    for (; kb < blocks; kb += kWaves) {
-        if (kb + kWaves < blocks) load(kb + kWaves, next);
-        multiply(kb, cur);
-        cur = next;
+    for (int kb = wave; kb < blocks; kb += kDepth * kWaves) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) {
+            const int at = kb + i * kWaves;
+            if (at >= blocks) break;
+            multiply(at, ring[i]);
+            if (at + kDepth * kWaves < blocks) load(at + kDepth * kWaves, ring[i]);
+        }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[wave][4 * q + e][r] = acc[e];
