@@ -61,13 +61,15 @@ __device__ __forceinline__ void for_each(F&& f, std::integer_sequence<int, I...>
 // column count or the LDS (shared by two workgroups) does not allow it
 constexpr int epilogue_columns(int NA, int NB) { return NA == 4 && NB % 2 == 0 ? 64 : 32; }
 
-// Epilogue of one wave, N % 8 == 0: 32 rows at a time are rounded, turned through the
+// Epilogue of one wave: 32 rows at a time are rounded, turned through the
 // wave's own LDS (`ep`) and stored as pieces of rows, 16 bytes a lane: 64 columns
 // are full 128-byte lines.  Lane l, r = l % 16, q = l / 16, holds of accumulator (i, j)
 // row 16 i + r, columns 16 j + 4 q .. + 3.  16-byte chunks are swizzled by the row, so
 // that neither side has bank conflicts.  Rows past M and columns past N are sent past
-// the end of the buffer, which drops them; every call issues 2 NA NB stores.
-template <int NA, int NB>
+// the end of the buffer, which drops them; every call issues at least 2 NA NB stores.
+// VEC: N % 8 == 0.  Else rows begin at any even address (memory takes such stores), and
+// the piece that N cuts is stored value by value.
+template <int NA, int NB, bool VEC>
 __device__ __forceinline__ void store_block_rows(const f32x4 (&acc)[2 * NA][2 * NB],
                                                  __amdgpu_buffer_rsrc_t rsY, int N, int row0,
                                                  int col0, char* ep) {
@@ -101,33 +103,21 @@ __device__ __forceinline__ void store_block_rows(const f32x4 (&acc)[2 * NA][2 * 
                 const u32x4 w = lds_read<u32x4>(ep, lr * kPitch + 16 * (och ^ swz(lr)));
                 const uint32_t o =
                     (uint32_t(row0 + 32 * a + lr) * uint32_t(N) + uint32_t(col)) * 2u;
-                __builtin_amdgcn_raw_buffer_store_b128(w, rsY, col < N ? o : 0xFFFFFFF0u, 0, 0);
+                const bool whole = col + 8 <= N;
+                __builtin_amdgcn_raw_buffer_store_b128(w, rsY, whole ? o : 0xFFFFFFF0u, 0, 0);
+                if constexpr (!VEC) {
+                    if (__builtin_amdgcn_ballot_w64(col < N && !whole) == 0) continue;
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        __builtin_amdgcn_raw_buffer_store_b16(
+                            uint16_t(w[e / 2] >> (16 * (e % 2))), rsY,
+                            !whole && col + e < N ? o + 2 * e : 0xFFFFFFF0u, 0, 0);
+                }
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
-}
-
-// Epilogue for other N: every lane stores its values one by one.
-template <int NA, int NB>
-__device__ __forceinline__ void store_block_single(const f32x4 (&acc)[2 * NA][2 * NB],
-                                                   __amdgpu_buffer_rsrc_t rsY, int N, int row0,
-                                                   int col0) {
-    const int l = fresh_lane();
-    const int r = l & 15, q = l >> 4;
-#pragma unroll
-    for (int i = 0; i < 2 * NA; ++i)
-#pragma unroll
-        for (int j = 0; j < 2 * NB; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int col = col0 + 16 * j + 4 * q + e;
-                const uint32_t o = (uint32_t(row0 + 16 * i + r) * uint32_t(N) + uint32_t(col)) * 2u;
-                __builtin_amdgcn_raw_buffer_store_b16(
-                    __builtin_bit_cast(uint16_t, static_cast<__bf16>(acc[i][j][e])), rsY,
-                    col < N ? o : 0xFFFFFFF0u, 0, 0);
-            }
 }
 
 // VEC: N % 8 == 0; ODD: a tile has an odd number of blocks, at least 3 (else an even
@@ -409,10 +399,7 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
             }
             block(S1{}, Other{}, AfterTail{}, AfterX{}, Late{}, All{}, np - 1);
         }
-        if constexpr (VEC)
-            store_block_rows<NA, NB>(acc, rsY, N, row0, col0, smem + kOffEp + wave * kEp);
-        else
-            store_block_single<NA, NB>(acc, rsY, N, row0, col0);
+        store_block_rows<NA, NB, VEC>(acc, rsY, N, row0, col0, smem + kOffEp + wave * kEp);
     }
     wait_vmcnt<0>();  // the loads past the last tile still write LDS
 }

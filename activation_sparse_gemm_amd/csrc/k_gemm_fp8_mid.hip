@@ -197,13 +197,9 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
         for (int j = 0; j < CN; ++j) {
             const int n = col0 + 16 * j + 4 * q;
             const f32x4& v = acc[i][j];
-            if ((N & 3) == 0) {  // then a group of 4 columns is inside N or outside
-                if (n < N)
-                    *reinterpret_cast<u32x2*>(y + n) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-            } else if ((N & 1) == 0) {
-                if (n < N) *reinterpret_cast<uint32_t*>(y + n) = pack_bf16x2(v[0], v[1]);
-                if (n + 2 < N) *reinterpret_cast<uint32_t*>(y + n + 2) = pack_bf16x2(v[2], v[3]);
+            if (n + 4 <= N) {
+                const u32x2 w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                __builtin_memcpy(y + n, &w, 8);  // one store, at any even address
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)

@@ -181,7 +181,9 @@ SHAPES = [(9, 3072, 8200), (16, 64, 9001), (190, 704, 9100), (190, 64, 9101), (5
           # 128x128, then few rows and many columns, and 64x128 two to a unit
           (100, 4160, 3000), (200, 320, 3003), (333, 576, 3004), (333, 64, 3000), (500, 448, 3000),
           (150, 320, 9101), (200, 704, 9101), (190, 64, 9104), (300, 2112, 9100), (350, 2176, 9001),
-          (20, 192, 40001), (50, 192, 40002), (160, 192, 18433), (160, 64, 18440)]
+          (20, 192, 40001), (50, 192, 40002), (160, 192, 18433), (160, 64, 18440),
+          # persistent 128x128 tiles with an odd number of K blocks
+          (2100, 640, 1551), (2100, 640, 1552), (2200, 576, 2000)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -195,7 +197,8 @@ def test_product_shapes(M, K, N):
 
 
 @pytest.mark.parametrize("M,K,N", [(4046, 640, 9100), (9216, 256, 3072), (4096, 3072, 12288),
-                                   (8192, 64, 8192), (5000, 448, 7001)])
+                                   (8192, 64, 8192), (5000, 448, 7001), (4608, 320, 4104),
+                                   (9216, 256, 3071), (3100, 256, 12001), (2050, 704, 12346)])
 def test_product_large_sampled_rows(M, K, N):
     q, s, xv = operand(M, K, 2)
     wq, ws, wv = weight(N, K, 9)
@@ -208,7 +211,7 @@ def test_product_large_sampled_rows(M, K, N):
 
 
 @pytest.mark.parametrize("M,K,N", [(8, 512, 40), (200, 384, 300), (1100, 640, 1030), (1700, 640, 1290),
-                                   (4100, 192, 4500)])
+                                   (4100, 192, 4500), (2100, 320, 1551), (9216, 192, 3071)])
 def test_product_exact_on_small_integers(M, K, N):
     """Integers in -8..8, unlike powers of two per block: every partial sum is exact in fp32 and
     the result checks lane, channel and scale assignment bit for bit."""
@@ -277,6 +280,32 @@ def test_layer_is_quantiser_then_product(M, K, N):
     check_product(Y, bo.values(*bo.quantize(x)), wv, f"layer {M}x{K}->{N}")
     Y2 = lynx.linear_fp8_packed(*lynx.quantize_fp8(X), wq, ws)
     assert torch.equal(Y.view(torch.int16), Y2.view(torch.int16))
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 64, 17), (60, 192, 33), (333, 576, 1003), (190, 704, 9101), (300, 2112, 9101),
+                                   (2100, 640, 1551), (4608, 320, 4101), (9101, 192, 3071)])
+def test_nothing_is_written_behind_the_outputs(M, K, N):
+    bits, _ = heavy(M, K, 1)
+    X = dev(bits)
+    wq, ws, _ = weight(N, K, 6)
+    tail = 1 << 16
+    say(f"fp8 memory behind the outputs M={M} K={K} N={N}")
+
+    def guarded(n, dtype, shape):
+        buf = torch.full((n + tail,), 0xA5, dtype=torch.uint8, device="cuda")
+        return buf, buf[:n].view(dtype).view(shape)
+    words = (K + 511) // 512
+    bq, q = guarded(M * K, FP8, (M, K))
+    bs, s = guarded(words * M * 4, E8M0, (words, M, 4))
+    by, Y = guarded(2 * M * N, torch.bfloat16, (M, N))
+    bz, Z = guarded(2 * M * N, torch.bfloat16, (M, N))
+    lynx.quantize_fp8(X, out=(q, s))
+    lynx.linear_fp8_packed(q, s, wq, ws, Y=Y)
+    lynx.linear_fp8(X, wq, ws, Y=Z)
+    torch.cuda.synchronize()
+    assert torch.equal(Y.view(torch.int16), Z.view(torch.int16))
+    for b in (bq, bs, by, bz):
+        assert bool((b[-tail:] == 0xA5).all())
 
 
 def test_empty_sizes():
