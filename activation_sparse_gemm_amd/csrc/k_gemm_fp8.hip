@@ -20,8 +20,10 @@
 //   B1 before its last two W fragments, which have been read: W of block p + 1 has
 //      landed; W's slot p is free and takes block p + 2, and X's slot p + 1, whose
 //      fragments are all in registers, takes block p + 3 in the next block.
-// A slot's loads have about a block's time (2048 cycles at NA = NB = 4) to land.  They
-// are spread over the block: in a burst they hold up the wave that issues them.
+// A slot's loads have about a block's time (2048 cycles at NA = NB = 4) to land, so they
+// are issued early, W's right after B1, but X's spread over the block: more of them at
+// once hold up the wave that issues them.  9216 x 12288 -> 3072 256 us; with half of W's
+// after the next block's start 264.
 //
 // The blocks run on across tiles: a tile's last two blocks load the next tile's
 // first two, in flight during the epilogue.  256 x 256 tiles (the loop for
@@ -68,13 +70,15 @@ constexpr int epilogue_columns(int NA, int NB) { return NA == 4 && NB % 2 == 0 ?
 // that neither side has bank conflicts.  Rows past M and columns past N are sent past
 // the end of the buffer, which drops them; every call issues at least 2 NA NB stores.
 // VEC: N % 8 == 0.  Else rows begin at any even address (memory takes such stores), and
-// the piece that N cuts is stored value by value.
+// the pieces that N cuts are kept in LDS and stored value by value at the end (from the
+// accumulators, or in between, the branches cost 28-51 spilled registers).
 template <int NA, int NB, bool VEC>
 __device__ __forceinline__ void store_block_rows(const f32x4 (&acc)[2 * NA][2 * NB],
                                                  __amdgpu_buffer_rsrc_t rsY, int N, int row0,
                                                  int col0, char* ep) {
     constexpr int kCols = epilogue_columns(NA, NB);
     constexpr int kChunks = kCols / 8, kPitch = 2 * kCols, kRows = 64 / kChunks;
+    constexpr int kCut = 32 * kPitch;
     const int l = fresh_lane();
     const int r = l & 15, q = l >> 4;
     auto swz = [](int row) { return kCols == 64 ? row & 7 : (row >> 1) & 3; };
@@ -100,24 +104,31 @@ __device__ __forceinline__ void store_block_rows(const f32x4 (&acc)[2 * NA][2 * 
 #pragma unroll
             for (int i = 0; i < 32 / kRows; ++i) {
                 const int lr = i * kRows + orow;
-                const u32x4 w = lds_read<u32x4>(ep, lr * kPitch + 16 * (och ^ swz(lr)));
+                const int at = lr * kPitch + 16 * (och ^ swz(lr));
                 const uint32_t o =
                     (uint32_t(row0 + 32 * a + lr) * uint32_t(N) + uint32_t(col)) * 2u;
                 const bool whole = col + 8 <= N;
+                const u32x4 w = lds_read<u32x4>(ep, at);
                 __builtin_amdgcn_raw_buffer_store_b128(w, rsY, whole ? o : 0xFFFFFFF0u, 0, 0);
-                if constexpr (!VEC) {
-                    if (__builtin_amdgcn_ballot_w64(col < N && !whole) == 0) continue;
-#pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        __builtin_amdgcn_raw_buffer_store_b16(
-                            uint16_t(w[e / 2] >> (16 * (e % 2))), rsY,
-                            !whole && col + e < N ? o + 2 * e : 0xFFFFFFF0u, 0, 0);
-                }
+                if constexpr (!VEC)  // the others' go to a place that is not read
+                    *reinterpret_cast<u32x4*>(
+                        ep + kCut + 16 * (!whole && col < N ? 32 * a + lr : 32 * NA)) = w;
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
+    if constexpr (!VEC) {
+        const int cut = N & ~7;
+        if (cut < col0 || cut >= col0 + 32 * NB) return;
+#pragma unroll 1
+        for (int row = l; row < 32 * NA; row += 64)
+#pragma unroll 1
+            for (int e = 0; e < N - cut; ++e)
+                __builtin_amdgcn_raw_buffer_store_b16(
+                    lds_read<uint16_t>(ep, kCut + 16 * row + 2 * e), rsY,
+                    (uint32_t(row0 + row) * uint32_t(N) + uint32_t(cut + e)) * 2u, 0, 0);
+    }
 }
 
 // VEC: N % 8 == 0; ODD: a tile has an odd number of blocks, at least 3 (else an even
@@ -136,13 +147,17 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     constexpr int kDmaX = 2 * NA + 1, kDmaW = 2 * NB;  // DMA instructions per wave and block
     constexpr int kRing = NB == 3 ? 3 : 4;          // W fragments in registers; divides NJ
     constexpr int kM = NI * NJ;                     // matrix instructions per wave and block
-    constexpr int kB0 = kM >= 64 ? 8 : 1, kB1 = (NJ - 2) * NI + 1; // the barriers follow these instructions
+    // The barriers follow these instructions
+    constexpr int kB0 = NA == 2 ? 1 : NB == 3 ? 8 : 12, kB1 = (NJ - 2) * NI + 1;
     constexpr int kRead = (NJ - 3) * NI + 1;        // X is read before this one
-    constexpr int kTailW = kDmaW / 2;               // loads of W issued after B1, the others next
-    constexpr int kLateW = kM >= 64 ? 13 : 6;       // ... before this instruction
-    constexpr int kEndX = kM >= 64 ? 40 : kM >= 48 ? 24 : kB1;  // X's loads are issued before this one
+    // X's loads are issued from this one (ODD: after B0, for the fragments that are read
+    // again at a tile's end) ...
+    constexpr int kFromX = ODD ? kB0 : NA == 2 ? 0 : 5;
+    constexpr int kEndX = NA == 2 ? kB1 : NB == 3 ? 32 : 48;  // ... and before this one
+    constexpr int kEarlyX = spare(NI, kFromX, kB0) * kDmaX / spare(NI, kFromX, kEndX);  // before B0
     constexpr int kStores = 2 * NA * NB;            // stores of an epilogue, at least
-    constexpr int kEp = 64 * epilogue_columns(NA, NB);  // a wave's LDS for the epilogue
+    // a wave's LDS for the epilogue
+    constexpr int kEp = 64 * epilogue_columns(NA, NB) + (VEC ? 0 : 16 * (32 * NA + 1));
     constexpr int kBS = NB == 3 ? NB : 1;           // scale blocks a wave's columns touch
     // rows of tiles that an XCD walks down together.  16384 x 4096 -> 4096 6 rows 201 us, 4
     // 208, 8 217; 9216 x 3072 -> 12288 270, 266, 274; 256 x 192 tiles, 6000 x 4096 -> 11008
@@ -152,9 +167,9 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     // span less than 2^31: kPast plus a row's offset does not wrap)
     constexpr uint32_t kPast = 0x80000000u;
     constexpr int kOffW = 2 * kX, kOffEp = 2 * kX + 2 * kW, kLds = kOffEp + 4 * kEp;
-    static_assert(NJ % kRing == 0 && kLateW < kEndX && kEndX <= kB1, "schedule");
+    static_assert(NJ % kRing == 0 && kEndX <= kB1 && kB0 < kRead, "schedule");
     static_assert(kLds <= 160 * 1024 / (NA == 4 ? 1 : 2), "LDS budget");
-    static_assert(kStores + kDmaX < 64 && kStores + kDmaW < 64, "vmcnt range");
+    static_assert(kStores + kDmaX < 64 && kStores + kDmaW + kEarlyX < 64, "vmcnt range");
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
 
     const int lane = threadIdx.x & 63;
@@ -232,11 +247,9 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     uint32_t atx = 0, ats = 0, atw = 0;  // and their offsets
     Aim next = {0, 0, 0};           // the next tile's
     // Block p on fragment set S: waits for X (B0) and W (B1) until at most wait0 and
-    // wait1 later vector memory operations are under way; issues `late` loads of W that
-    // the block before left, X's loads, and `tail` loads of W.
-    auto block = [&](auto set, auto first, auto wait0, auto wait1, auto late, auto tail, int p) {
+    // wait1 later vector memory operations are under way; issues X's loads, then W's.
+    auto block = [&](auto set, auto first, auto wait0, auto wait1, int p) {
         constexpr int S = decltype(set)::value;
-        constexpr int kLate = decltype(late)::value, kTail = decltype(tail)::value;
         const int oth = 1 - slot;
         const int shift = 8 * (p & 3);                    // the block's byte in the scale words
         // 2^-127 for the channels it is filled up with
@@ -292,15 +305,9 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
                     }
                 }, std::make_integer_sequence<int, (t + 1) * n / g - t * n / g>{});
             }
-            // ... and the loads: the rest of W, X, the first of W after B1
-            if constexpr (!w_read && kLate > 0 && k < kLateW) {
-                constexpr int g = spare(NI, 0, kLateW), t = spare(NI, 0, k);
-#pragma unroll
-                for (int n = t * kLate / g; n < (t + 1) * kLate / g; ++n)
-                    dma_w(oth * kW, atw, lpw, kDmaW - kLate + n);
-            }
-            if constexpr (!w_read && k >= kLateW && k < kEndX) {
-                constexpr int g = spare(NI, kLateW, kEndX), t = spare(NI, kLateW, k);
+            // ... and the loads
+            if constexpr (!w_read && k >= kFromX && k < kEndX) {
+                constexpr int g = spare(NI, kFromX, kEndX), t = spare(NI, kFromX, k);
 #pragma unroll
                 for (int n = t * kDmaX / g; n < (t + 1) * kDmaX / g; ++n)
                     dma_x(slot * kX, atx, ats, lpx, n);
@@ -309,10 +316,10 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
                 lpw = lpx;
                 atw = over ? next.w : atw;
             }
-            if constexpr (!w_read && kTail > 0 && k > kB1) {
+            if constexpr (!w_read && k > kB1) {
                 constexpr int g = spare(NI, kB1 + 1, kM), t = spare(NI, kB1 + 1, k);
 #pragma unroll
-                for (int n = t * kTail / g; n < (t + 1) * kTail / g; ++n)
+                for (int n = t * kDmaW / g; n < (t + 1) * kDmaW / g; ++n)
                     dma_w(slot * kW, atw, lpw, n);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -339,8 +346,7 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
 #pragma unroll
         for (int i = 0; i < kDmaW; ++i) dma_w(p * kW, atw, p, i);
     }
-    wait_vmcnt<0>();  // both: no stores stand between them and the first waits (with ODD the
-                      // first block loads half of W's block 1 again)
+    wait_vmcnt<0>();  // both: no stores stand between them and the first waits
     block_barrier();
 #pragma unroll
     for (int n = 0; n < 2 * NI; ++n) read(offX + (n / 2) * 16 * kRow, x[0][n / 2], n % 2);
@@ -348,22 +354,19 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
     for (int n = 0; n < 4; ++n) read(offW + (n / 2) * 16 * kRow, w[n / 2], n % 2);
 #pragma unroll
     for (int i = 0; i < NI; ++i) sx[i] = lds_read<uint32_t>(smem, offS + i * 64);
+    wait_lgkm0();
+    block_barrier();  // the first block loads into X's slot before its B0
 
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
     using First = std::true_type;
     using Other = std::false_type;
-    using AfterTail = std::integral_constant<int, kTailW>;      // of W, after X's last load
-    using AfterX = std::integral_constant<int, kDmaX>;          // of X, after W's last load
+    using AfterW = std::integral_constant<int, kDmaW + kEarlyX>;  // and this block's first of X
+    using AfterX = std::integral_constant<int, kDmaX>;
     // a tile's first waits pass over the last one's stores: its first two blocks were
-    // loaded before them, W of block 1 wholly
-    using Stores0 = std::integral_constant<int, kDmaW + kStores>;
+    // loaded before them
+    using Stores0 = std::integral_constant<int, kDmaW + kEarlyX + kStores>;
     using Stores1 = std::integral_constant<int, kDmaX + kStores>;
-    using OddStores0 = std::integral_constant<int, kTailW + kStores>;
-    using Tail = std::integral_constant<int, kTailW>;
-    using Late = std::integral_constant<int, kDmaW - kTailW>;
-    using All = std::integral_constant<int, kDmaW>;
-    using None = std::integral_constant<int, 0>;
     for (int v = blockIdx.x; v < ntiles; v += gridDim.x) {
         int tm, tn;
         tile_of(v, tiles_m, tiles_n, tm, tn, kGroup);
@@ -376,14 +379,12 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
         for (int b = 0; b < kBS; ++b) sw[b] = wsp[b][0];
         next = aim(v + int(gridDim.x));
         lpx = lpw = 1;  // block p loads block p + 2, or the next tile's p + 2 - np
+        block(S0{}, First{}, Stores0{}, Stores1{}, 0);
         if constexpr (ODD) {
-            // W of block 1 is half loaded after the last tile's stores, so that all pairs of
-            // blocks are alike and the registers suffice
-            block(S0{}, First{}, OddStores0{}, AfterX{}, Late{}, Tail{}, 0);
             int p = 1;
             do {
-                block(S1{}, Other{}, AfterTail{}, AfterX{}, Late{}, Tail{}, p);
-                block(S0{}, Other{}, AfterTail{}, AfterX{}, Late{}, Tail{}, p + 1);
+                block(S1{}, Other{}, AfterW{}, AfterX{}, p);
+                block(S0{}, Other{}, AfterW{}, AfterX{}, p + 1);
                 p += 2;
             } while (p < np);
             // the next tile begins with set 0 again: its fragments now that it is free (their
@@ -392,12 +393,11 @@ __global__ __launch_bounds__(NT, NA == 4 ? 1 : 2) void gemm_fp8_tiled(
             for (int n = 0; n < 2 * NI; ++n)
                 read(offX + slot * kX + (n / 2) * 16 * kRow, x[0][n / 2], n % 2);
         } else {
-            block(S0{}, First{}, Stores0{}, Stores1{}, None{}, Tail{}, 0);
             for (int p = 1; p < np - 2; p += 2) {
-                block(S1{}, Other{}, AfterTail{}, AfterX{}, Late{}, Tail{}, p);
-                block(S0{}, Other{}, AfterTail{}, AfterX{}, Late{}, Tail{}, p + 1);
+                block(S1{}, Other{}, AfterW{}, AfterX{}, p);
+                block(S0{}, Other{}, AfterW{}, AfterX{}, p + 1);
             }
-            block(S1{}, Other{}, AfterTail{}, AfterX{}, Late{}, All{}, np - 1);
+            block(S1{}, Other{}, AfterW{}, AfterX{}, np - 1);
         }
         store_block_rows<NA, NB, VEC>(acc, rsY, N, row0, col0, smem + kOffEp + wave * kEp);
     }

@@ -14,10 +14,11 @@
 //
 // A workgroup takes 16 columns; its 8 waves take the K blocks in turn, straight
 // from global memory into registers: per 16 rows and block two loads of 16 bytes a
-// lane, each 64 contiguous bytes of 16 rows, three blocks under way (from HBM: 2 x 3072
-// -> 18432 12.8 us = 4.4 TB/s, two blocks 14.4; 1 x 12288 -> 3072 11.5 and 14.1; 16 waves
-// 13.8 and 11.5; from the cache 11.2 and 12.3).  The waves' sums are joined through LDS in wave order, so the result
-// does not depend on timing.
+// lane, each 64 contiguous bytes of 16 rows, three blocks under way.  From HBM, in us
+// (one block ahead, 16 waves): 2 x 3072 -> 18432 12.8 = 4.4 TB/s (14.4, 13.8); 1 x 12288
+// -> 3072 11.5 (14.1, 11.5); from the cache the first takes 11.2 (12.3, 12.3).  The
+// waves' sums are joined through LDS in wave order, so the result does not depend on
+// timing.
 //
 // QUANT reads bf16 X and quantises it first, as lynx_quantize_fp8 does, into LDS: 16
 // lanes a row's block.  Every workgroup repeats that, so it is used where X is small

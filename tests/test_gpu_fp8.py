@@ -308,6 +308,23 @@ def test_nothing_is_written_behind_the_outputs(M, K, N):
         assert bool((b[-tail:] == 0xA5).all())
 
 
+def test_debug_mode_changes_no_byte(monkeypatch):
+    bits, _ = heavy(60, 576, 3)
+    X = dev(bits)
+    W = dev(heavy(200, 576, 5)[0])
+
+    def results():
+        wq, ws = lynx.quantize_fp8_weight(W)
+        q, s = lynx.quantize_fp8(X)
+        h, hs = lynx.norm_modulate(X, "layer", fp8=True)
+        out = [wq, ws, q, s, h, hs, lynx.linear_fp8(X, wq, ws), lynx.linear_fp8_packed(h, hs, wq, ws)]
+        return [t.contiguous().view(torch.uint8).clone() for t in out]
+    say("fp8 and norms in debug mode")
+    plain = results()
+    monkeypatch.setenv("LYNX_DEBUG", "1")
+    assert all(torch.equal(a, b) for a, b in zip(plain, results()))
+
+
 def test_empty_sizes():
     wq, ws, _ = weight(40, 64, 1)
     x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
