@@ -269,7 +269,7 @@ def test_product_extreme_scales():
                                    (16, 704, 8191), (33, 64, 40), (4100, 320, 64), (2049, 2240, 70), (500, 192, 2000),
                                    (1000, 2048, 700), (40, 1984, 5000), (18, 448, 8192),
                                    (16, 2112, 8200), (3, 10880, 50), (16, 64, 33), (40, 1472, 70), (300, 640, 520),
-                                   (1300, 448, 1100)])
+                                   (1300, 448, 1100), (9100, 192, 64), (8200, 704, 120), (70, 192, 10900), (30, 64, 30000)])
 def test_layer_is_quantiser_then_product(M, K, N):
     bits, x = heavy(M, K, M)
     wq, ws, wv = weight(N, K, 3)
