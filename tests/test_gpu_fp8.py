@@ -325,6 +325,31 @@ def test_debug_mode_changes_no_byte(monkeypatch):
     assert all(torch.equal(a, b) for a, b in zip(plain, results()))
 
 
+@pytest.mark.parametrize("M,K,N", [(5, 576, 40), (60, 192, 300), (300, 704, 2000), (100, 4160, 3000), (300, 2240, 9100),
+                                   (2100, 576, 1552), (4608, 320, 4104), (4097, 64, 4104), (9100, 320, 3079)])
+def test_unused_scales_do_not_matter_and_nan_codes_stay_in_their_row(M, K, N):
+    q, s, _ = operand(M, K, 1)
+    wq, ws, _ = weight(N, K, 2)
+    say(f"fp8 unused scales M={M} K={K} N={N}")
+    ref = lynx.linear_fp8_packed(q, s, wq, ws)
+    kb = -(-K // 128)
+    sb, wb = u8(s).copy(), u8(ws).copy()
+    for b in range(kb, 4 * sb.shape[0]):
+        sb[b // 4, :, b % 4] = 255
+        wb[:, b] = 255
+    Y = lynx.linear_fp8_packed(q, e8_dev(sb), wq, e8_dev(wb))
+    assert torch.equal(Y.view(torch.int16), ref.view(torch.int16))
+    row, col = M // 2, N - 1
+    q.view(torch.uint8)[row, K - 1] = 0x7F          # e4m3's NaN, in the last block's end ...
+    wq.view(torch.uint8)[col, K - 64] = 0xFF        # ... and in W
+    Y = lynx.linear_fp8_packed(q, s, wq, ws)
+    bad = torch.isnan(Y)
+    want = torch.zeros_like(bad)
+    want[row] = True
+    want[:, col] = True
+    assert torch.equal(bad, want) and torch.equal(Y[~bad], ref[~bad])
+
+
 def test_empty_sizes():
     wq, ws, _ = weight(40, 64, 1)
     x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
@@ -361,7 +386,8 @@ def test_python_checks_name_the_argument():
         lynx.quantize_fp8(torch.zeros((2, 96), dtype=torch.bfloat16, device="cuda"))
 
 
-@pytest.mark.parametrize("M,K,N", [(2, 512, 300), (60, 640, 256), (1100, 512, 1030)])
+@pytest.mark.parametrize("M,K,N", [(2, 512, 300), (60, 640, 256), (1100, 512, 1030), (300, 2176, 9100), (2200, 576, 2000),
+                                   (2100, 1024, 1551), (4608, 640, 4104), (4608, 512, 4101), (9216, 1024, 3072)])
 def test_repeated_calls_two_streams_and_graph_replays_agree(M, K, N):
     bits, _ = heavy(M, K, 8)
     X = dev(bits)
