@@ -36,12 +36,17 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
     constexpr int kX = TM * (QUANT ? 256 : 128), kW = TN * 128;
     constexpr int kGroup = kX + kW + (QUANT ? 0 : 1024);  // one block: + a scale word per row of X
     constexpr int kSlot = KG * kGroup;
+    // W's scale word (a tile's columns lie in one scale block) comes with the step, behind
+    // X's, by wave 3, where the step is short: a scalar load under way makes every wait for
+    // LDS reads a wait for it too.  64 x 12288 -> 3072 14.0 us, 15.1 with scalar loads; but
+    // 1000 x 12288 -> 3072 53.2 and 51.7, QUANT 333 x 1024 -> 1024 6.4 and 6.2.
+    constexpr bool kStepW = !QUANT && RM * CN <= 4;
     // per wave and step
     constexpr int kDmaX = QUANT ? 2 * RM : RM, kDmaW = CN, kDma = kDmaX + kDmaW + (QUANT ? 0 : 1);
     constexpr int kJoin = (KG - 1) * TM * TN * 4;
     constexpr int kQ = QUANT ? TM * 128 + TM : 0;         // a group's quantised block and scales
     constexpr int kLds = SLOTS * kSlot + KG * kQ;
-    static_assert(TM <= 256 && kLds <= 160 * 1024 && kJoin <= SLOTS * kSlot, "LDS budget");
+    static_assert(TM <= 128 && TN <= 128 && kLds <= 160 * 1024 && kJoin <= SLOTS * kSlot, "LDS budget");
     static_assert((SLOTS - 2) * kDma < 64, "vmcnt range");
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
 
@@ -61,7 +66,10 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
     const uint32_t lds0 = lds_addr(smem) + uint32_t(group * kGroup);
     const i32x4 rsX = make_rsrc(X, uint32_t(M) * uint32_t(K) * (QUANT ? 2u : 1u));
     const i32x4 rsW = make_rsrc(Wq, uint32_t(N) * uint32_t(K));
-    const i32x4 rsS = make_rsrc(Xs, uint32_t(words) * uint32_t(M) * 4u);
+    const bool wscale = kStepW && wave == 3;
+    const i32x4 rsS = wscale ? make_rsrc(Ws, uint32_t(nblocks) * uint32_t(words) * 4u)
+                             : make_rsrc(Xs, uint32_t(words) * uint32_t(M) * 4u);
+    const uint32_t wordS = wscale ? 4u : uint32_t(M) * 4u;  // from a word to the next
     // DMA instruction j of wave w moves rows 8 w + l/8 + 32 j, lane l's 16 bytes the
     // chunk that the row's swizzle puts there (the same for every j)
     const int lrow = 8 * wave + (lane >> 3);
@@ -72,7 +80,8 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
                               : uint32_t(tm * TM + lrow) * uint32_t(K) + uint32_t(16 * chunk);
     const uint32_t vw = uint32_t(tn * TN + lrow) * uint32_t(K) + uint32_t(16 * chunk);
     // rows past the end take the last row's words (the word's offset is not range checked)
-    const uint32_t vs = uint32_t(min(tm * TM + (64 * wave) % TM + lane, M - 1)) * 4u;
+    const uint32_t vs = wscale ? uint32_t(tn * TN / kFp8Block * words) * 4u
+                               : uint32_t(min(tm * TM + (64 * wave) % TM + lane, M - 1)) * 4u;
     auto load = [&](int step, int slot) {  // past the last step: the last block again
         const uint32_t base = lds0 + uint32_t(slot * kSlot);
         const int kb = min(step * KG + group, blocks - 1);
@@ -93,15 +102,16 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
             dma16(base + kX + 1024 * (wave + 4 * j), vw - back + uint32_t(32 * j) * uint32_t(K), rsW,
                   off);
         if constexpr (!QUANT)
-            dma4(base + kX + kW + 256 * wave, vs, rsS, uint32_t(kb >> 2) * uint32_t(M) * 4u);
+            dma4(base + kX + kW + 256 * wave, vs, rsS, uint32_t(kb >> 2) * wordS);
     };
 #pragma unroll
     for (int s = 0; s < SLOTS - 1; ++s) load(s, s);
 
-    static_assert(128 % (16 * CN) == 0, "a wave's columns lie in one scale block of W");
+    static_assert(128 % TN == 0, "a tile's columns lie in one scale block of W");
+    const uint32_t* wsp = Ws + size_t(tn * TN / kFp8Block) * size_t(words);
+    uint32_t ws = 0;
+    if constexpr (!kStepW) ws = wsp[min(group >> 2, words - 1)];
     const int row0 = tm * TM + wm * 16 * RM, col0 = tn * TN + wn * 16 * CN;
-    const uint32_t* wsp = Ws + size_t(__builtin_amdgcn_readfirstlane(
-                                   min(col0 / kFp8Block, nblocks - 1))) * size_t(words);
     const int sw = fp8_swz(r);
     char* const xq = smem + SLOTS * kSlot + group * kQ;      // QUANT: the group's values ...
     uint8_t* const xs = reinterpret_cast<uint8_t*>(xq + TM * 128);  // ... and scales
@@ -117,7 +127,6 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
     int slot = 0;
     for (int step = 0; step < steps; ++step) {
         const int kb = step * KG + group;
-        const uint32_t ws = wsp[min(kb >> 2, words - 1)];
         wait_vmcnt_lgkm0<(SLOTS - 2) * kDma>();  // this step has landed, the last one's reads are done
         block_barrier();
         load(step + SLOTS - 1, slot == 0 ? SLOTS - 1 : slot - 1);
@@ -134,6 +143,7 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
         };
 #pragma unroll
         for (int j = 0; j < CN; ++j) w[j] = frag(s, offW + j * 16 * 128, upper);
+        if constexpr (kStepW) ws = lds_read<uint32_t>(s, group * kGroup + kX + kW + 3 * 256);
         if constexpr (QUANT) {
             const bool in = kb * kFp8Block + 8 * r < K;  // channels past K count as zeros
 #pragma unroll
@@ -165,6 +175,7 @@ __global__ __launch_bounds__(256 * KG) void gemm_fp8_mid(
             for (int j = 0; j < CN; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     w[j], x[i], acc[i][j], 0, 0, 0, int(sws), 0, int(sx[i]));
+        if constexpr (!kStepW) ws = wsp[min((kb + KG) >> 2, words - 1)];
         slot = slot == SLOTS - 1 ? 0 : slot + 1;
     }
     wait_vmcnt_lgkm0<0>();  // the loads past the last step write LDS too
