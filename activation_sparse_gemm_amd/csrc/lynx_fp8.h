@@ -109,15 +109,17 @@ inline int64_t fp8_tiles(int64_t M, int64_t N, int64_t tm, int64_t tn) {
 // Whether lynx_linear_fp8 quantises inside the product, in the same order of sums as the
 // product has on a 256-unit device (so that its results are those of quantiser and
 // product).  It costs a product 1.4 us per 1024 of K in 32 x 32 tiles, 2.1 in 32 x 64 ones
-// and 3.6 with two of them to a unit, and saves a kernel (2.2 us and its launch) and 0.55
-// us per million elements of X, which is then read once: worth it for short K or many
-// rows.  In one kernel and apart: 64 x 1024 -> 1024 5.6 and 6.4 us, 64 x 2048 -> 2048 8.4
-// and 7.6; 128 x 1024 -> 4096 6.7 and 7.1; 768 x 1024 -> 1024 8.9 and 8.0, 9216 x 640 ->
-// 64 7.6 and 10.6; 4096 x 3072 -> 64 11.1 and 15.0.
+// and 3.6 with two of them to a unit, and saves 0.55 us per million elements of X, which
+// is then read once, and a kernel: 2.2 us, and 3 us of the host (5 with the workspace,
+// from Python), which bound short calls unless they are replayed from a graph.  1.3 us
+// are counted for that.  In one kernel and apart, us: from a graph 64 x 1024 -> 1024 5.6
+// and 6.4, 64 x 2048 -> 2048 8.3 and 7.4 (called one by one 7.9 and 11.6), 128 x 1472 ->
+// 3072 7.9 and 7.8 (7.4 and 11.6), 768 x 1024 -> 1024 8.8 and 7.9, 9216 x 640 -> 64 7.2 and
+// 10.4; 4096 x 3072 -> 64 11.0 and 15.0.
 enum class Fp8Fuse { no, few, mid32, mid64 };
 inline Fp8Fuse fp8_fuse(int64_t M, int64_t N, int64_t K) {
     if (fp8_is_few(M, N)) return M * K <= kFewQuant ? Fp8Fuse::few : Fp8Fuse::no;
-    const int64_t apart = 2200000 + M * K * 11 / 20;  // picoseconds
+    const int64_t apart = 3500000 + M * K * 11 / 20;  // picoseconds
     if (fp8_tiles(M, N, 32, 32) <= 256) return K * 1400 < apart ? Fp8Fuse::mid32 : Fp8Fuse::no;
     const int64_t tiles = fp8_tiles(M, N, 32, 64);
     if (tiles <= 512 && K * (tiles <= 256 ? 2050 : 3600) < apart) return Fp8Fuse::mid64;

@@ -34,7 +34,7 @@ def test_workspace_bytes():
     # few rows and few tiles are quantised inside the product
     assert ws(8, 100, 4096) == 0 and ws(1, 18432, 12288) == 0 and ws(16, 8191, 2048) == 0
     assert ws(300, 1024, 1024) == 0 and ws(4096, 64, 3072) == 0 and ws(17, 16, 64) == 0
-    assert ws(8, 100, 4160) > 0 and ws(16, 8192, 2112) > 0 and ws(300, 1024, 2112) > 0
+    assert ws(8, 100, 4160) > 0 and ws(16, 8192, 2560) > 0 and ws(300, 1024, 2112) > 0
     assert ws(0, 16, 64) == 0 and ws(4, 16, 100) == 0 and ws(-1, 16, 64) == 0
 
 
