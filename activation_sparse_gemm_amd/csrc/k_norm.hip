@@ -166,8 +166,10 @@ __global__ __launch_bounds__(64 * W) void block_norm_kernel(const NormArgs A) {
         if constexpr (HASY) {
             p.a1 = factor(A.gate ? A.gate + size_t(sample) * size_t(A.gate_stride) : nullptr, ch);
             p.a0 = term(A.post_bias, ch);
+            if (A.post_bias) {  // an absent one stays no term: 0 * inf is NaN
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p.a0.f[j] *= p.a1.f[j];
+                for (int j = 0; j < 8; ++j) p.a0.f[j] *= p.a1.f[j];
+            }
             const Vec8 w = factor(A.post_weight, ch);
 #pragma unroll
             for (int j = 0; j < 8; ++j) p.a1.f[j] *= w.f[j];
@@ -179,7 +181,7 @@ __global__ __launch_bounds__(64 * W) void block_norm_kernel(const NormArgs A) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             p.b1.f[j] += 1.f;
-            p.b0.f[j] = fmaf(p.b0.f[j], p.b1.f[j], t.f[j]);
+            p.b0.f[j] = A.bias ? fmaf(p.b0.f[j], p.b1.f[j], t.f[j]) : t.f[j];
             p.b1.f[j] *= w.f[j];
         }
         return p;

@@ -302,7 +302,10 @@ lynx_status lynx_linear_fp8_packed(const uint8_t* Xq, const uint8_t* Xs, const u
  * over the C channels of a row, with an absent (NULL) weight, scale or gate read
  * as no factor and an absent bias or shift as no term.  Rows are samples of
  * M / samples rows each, b the row's sample.  All arithmetic is fp32, and h is
- * taken from x' before x' is rounded for x_out.
+ * taken from x' before x' is rounded for x_out.  A channel's given parameters are
+ * combined first, into one factor and one term: weight * (1 + scale) and
+ * bias * (1 + scale) + shift, post_weight * gate and post_bias * gate.  So where one
+ * of them is infinite, a given bias of the other sign (or 0) makes NaN.
  *   - y == NULL: no branch; x' = x, and x_out, gate, post_weight and post_bias are
  *     NULL and residual_scale is not used.
  *   - h is written as bf16 to `h`, or as the 8-bit operand (quantised from the
