@@ -96,7 +96,9 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
     }
 }
 
-// v becomes v - mean (layer norm); returns 1 / sqrt(mean square + eps)
+// v becomes v - mean (layer norm); returns 1 / sqrt(mean square + eps), or NaN where the
+// sum of squares is not finite: rsqrt(inf) = 0 would turn a row that holds an infinity, or
+// squares past fp32's range, into zeros that nobody notices
 template <int W, int NV>
 __device__ __forceinline__ float normalise(Vec8 (&v)[NV], const bool (&in)[NV], int kind, float inv_c,
                                            float eps, float* slots) {
@@ -118,7 +120,8 @@ __device__ __forceinline__ float normalise(Vec8 (&v)[NV], const bool (&in)[NV], 
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) s = fmaf(v[i].f[j], v[i].f[j], s);
-    return rsqrtf(fmaf(row_sum<W>(s, slots + 4 * W), inv_c, eps));
+    const float sum = row_sum<W>(s, slots + 4 * W);
+    return sum < INFINITY ? rsqrtf(fmaf(sum, inv_c, eps)) : __builtin_nanf("");
 }
 
 template <int W, int NV, bool XF32, bool HASY>

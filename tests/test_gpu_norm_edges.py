@@ -77,3 +77,64 @@ def test_infinite_scale_without_a_bias(norm, shift):
     assert np.array_equal(byte, np.where(bad, 255, refb))
     same = ~bad.repeat(128, 1)
     assert np.array_equal(q[same], refq[same])
+
+
+# ---- rows that are not finite ------------------------------------------------------
+
+SIZES = [64, 640, 2048, 4096, 8200]   # 1, 2, 4 and 8 waves a row, and 3 vectors a lane
+BAD = [1, 2, 3, 5, 6]                 # rows of spoil() that a norm makes NaN
+
+
+def spoil(t):
+    """Rows with an infinity, a NaN, one value and many values whose squares pass fp32's range;
+    row 7 is large and in range."""
+    C = t.shape[1]
+    t[1, C // 3], t[2, C - 1], t[3, 5] = INF, -INF, NAN
+    t[5, C // 2] = 3e19
+    t[6] *= 2.0 ** 64
+    t[7, 9] = 2.0 ** 60
+    return t
+
+
+def whole_row(t, rows):
+    """The rows of t that are NaN throughout are these, and the others are finite."""
+    want = torch.zeros(t.shape, dtype=torch.bool, device="cuda")
+    want[rows] = True
+    return bool(torch.equal(torch.isnan(t), want)) and bool(torch.isfinite(t[~want]).all())
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("C", SIZES)
+def test_a_row_that_is_not_finite_becomes_nan(C, f32, norm):
+    x = ordinary(9, C, 1, f32)
+    ref = lynx.norm_modulate(x, norm)
+    x = spoil(x)
+    say(f"non-finite rows {norm} C={C} f32={f32}")
+    h = lynx.norm_modulate(x, norm)
+    assert whole_row(h, BAD)
+    same = [0, 4, 8]
+    assert torch.equal(h[same].view(torch.int16), ref[same].view(torch.int16))
+    if C % 64 == 0:
+        s = u8(lynx.norm_modulate(x, norm, fp8=True)[1])
+        kb = -(-C // 128)
+        byte = s.transpose(1, 0, 2).reshape(9, -1)[:, :kb]
+        assert (byte[BAD] == 255).all() and not (np.delete(byte, BAD, 0) == 255).any()
+
+
+@pytest.mark.parametrize("post", [None, "rms", "layer"])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("C", SIZES)
+def test_a_branch_that_is_not_finite(C, f32, post):
+    """A post norm makes all of x' NaN; without one x' holds the branch's value in its channel."""
+    x, y = ordinary(9, C, 1, f32), spoil(ordinary(9, C, 2))
+    say(f"non-finite branch {post} C={C} f32={f32}")
+    for norm in (None, "rms", "layer"):
+        xo, h = lynx.residual_norm(x, y, post_norm=post, norm=norm)
+        if post:
+            assert whole_row(xo, BAD)
+        else:
+            assert torch.equal(torch.isfinite(xo), torch.isfinite(y))
+            assert torch.equal(torch.isnan(xo), torch.isnan(y))
+        if norm:
+            assert whole_row(h, BAD)
