@@ -3,7 +3,14 @@
 //   z  = post(y),  x' = rho x + gate z,  h = pre(x') w + b,  h (1 + scale) + shift
 // in one pass over the rows: a row is read once, held in registers as fp32
 // through both norms, and x' and h (bf16, or the 8-bit operand) are written
-// once.  HBM traffic is what bounds it.
+// once.  HBM traffic is what bounds it, at 512 <= C <= 12288.  Two exceptions:
+//   - C > 12288 with y: the row, the next row and 32 floats of parameters to a vector do
+//     not fit the 256 registers that 8 waves a workgroup leave.  <8, 4> spills 64 of them
+//     (fp32 x: 95), and 4096 x 16384 takes 230 us (344) = 2.3 TB/s, 4096 x 12288 94 (138)
+//     = 4.3.  <8, 3> with fp32 x spills 10.
+//   - Narrow rows: a wave holds one row and one more ahead, so at C = 128 16 of 64 lanes
+//     work and few bytes are under way.  With y, 221184 x 128 takes 84 us = 2.7 TB/s, x 256
+//     101 = 4.5, 55296 x 512 43 = 5.3.
 //
 // A workgroup of W waves takes a run of consecutive rows, so that a sample's
 // parameters stay in registers from row to row (read anew per row they are as much
