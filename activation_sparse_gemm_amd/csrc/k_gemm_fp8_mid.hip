@@ -12,9 +12,9 @@
 // X, rows 4 q .. 4 q + 3 of W).  Channels past K are loaded again from inside the row:
 // the upper half of a last block of 64 is zeroed in W, blocks that fill up a step are
 // weighted 2^-127 in both operands, whose products are zero in fp32.  (A lane's
-// scale is not that of the lane's own channels but of a 32-channel piece of the
-// instruction's, so scales cannot mask half a block here.)  The groups' sums are
-// joined through LDS in order.
+// scale is that of the instruction's channels 32 q .. 32 q + 31, not of the lane's own
+// two chunks: the scales of lanes q >= 2 could mask the upper half as well, as
+// k_gemm_fp8.hip does.)  The groups' sums are joined through LDS in order.
 //
 // QUANT reads bf16 X and quantises it on the way, as lynx_quantize_fp8 does: a step's
 // rows land as they are (256 bytes a block) and 16 lanes turn a row's block into its
