@@ -1,9 +1,9 @@
 """The block norms against the fp64 oracle.
 
 Tolerances, per element (A: the sum of the magnitudes of an output's terms, which
-the oracle gives): fp32 sums of a lane's up to 64 values and a tree over at most
-256 lanes round at most 74 times, products and the root a few times more, so the
-arithmetic is off by at most 128 2^-24 A = 2^-17 A; a bf16 store adds 2^-8 |v|, an
+the oracle gives): fp32 sums of a lane's up to 32 values and a tree over at most
+512 lanes round at most 41 times, products and the root a few times more, so the
+arithmetic is off by less than 128 2^-24 A = 2^-17 A; a bf16 store adds 2^-8 |v|, an
 fp32 store 2^-24 |v|.  8-bit values add half a step: 2^-4 |v|, or 2^-10 of the
 scale for subnormals.  Without any norm x' has three roundings: 2^-22 A.
 """
