@@ -314,10 +314,10 @@ lynx_status lynx_linear_fp8_packed(const uint8_t* Xq, const uint8_t* Xs, const u
  *   - x and x_out are bf16, or fp32 where x_fp32 is not 0.  x_out may be x; no
  *     other output may overlap an input.
  *   - A norm makes a row NaN throughout (h, with every scale of the 8-bit form; after
- *     a post norm x' too) where what it is taken of holds a NaN or an infinity, or is so
- *     large that the sum of its squares, or for the mean of its values, passes fp32's
- *     range (a value of 1.9e19 does, or many smaller ones).  Where y has no post norm, a
- *     NaN or an infinity in x or y makes x' so in its channel alone.  No other row changes.
+ *     a post norm x' too) where the row it is taken of holds a NaN or an infinity, or
+ *     values so large that a sum of them or of their squares passes fp32's range (one of
+ *     2e19 does, or many smaller ones).  Where y has no post norm, a NaN or an infinity in
+ *     x or y makes x' so in its channel alone.  No other row changes.
  * Limits: C a multiple of 8, 8 <= C <= 16384; 0 <= M <= 2^23 (0 is a no-op);
  * samples >= 1 divides M; strides (in elements, from one sample's row to the
  * next; 0 = one row for all) >= 0 and multiples of 8; eps and post_eps >= 0.
