@@ -3,14 +3,16 @@
 Python face of liblynx.so: `sparsify`, `linear_sparse_lora`,
 `linear_sparse_lora_packed`, `linear_sparse_lora_noalloc`, `linear_dense`, the
 8-bit layer (`quantize_fp8`, `quantize_fp8_weight`, `linear_fp8`,
-`linear_fp8_packed`) and the block norms (`norm_modulate`, `residual_norm`) take
-torch device tensors and call the library's HIP kernels on torch's current
-stream.
+`linear_fp8_packed`), the block norms (`norm_modulate`, `residual_norm`), rotary
+positions (`qk_rotary`) and `attention` take torch device tensors and call the
+library's HIP kernels on torch's current stream.
 """
 from ._abi import (  # noqa: F401
     LIB_PATH,
     SCRATCH_BYTES,
     LynxError,
+    attention,
+    attention_workspace_bytes,
     fp8_workspace_bytes,
     lib,
     linear_dense,
@@ -22,6 +24,7 @@ from ._abi import (  # noqa: F401
     linear_sparse_lora_noalloc,
     linear_sparse_lora_packed,
     norm_modulate,
+    qk_rotary,
     quantize_fp8,
     quantize_fp8_weight,
     residual_norm,

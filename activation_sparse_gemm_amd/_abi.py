@@ -54,6 +54,45 @@ _NORM = struct.Struct("@13P6q3f3i")
 assert _NORM.size == ctypes.sizeof(Norm)
 
 
+PAIR_KINDS = {"adjacent": 0, "halves": 1}
+LADDER_KINDS = {"axis": 0, "joint": 1}
+
+
+class Rotary(ctypes.Structure):
+    """struct lynx_rotary (include/lynx.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in
+                 ("q", "k", "q_weight", "k_weight", "positions", "q_out", "k_out")]
+                + [(n, ctypes.c_int64) for n in
+                   ("tokens", "q_heads", "k_heads", "head_dim", "q_stride", "q_head_stride",
+                    "k_stride", "k_head_stride", "q_out_stride", "q_out_head_stride",
+                    "k_out_stride", "k_out_head_stride")]
+                + [("theta", ctypes.c_double), ("axis_dims", ctypes.c_int32 * 4)]
+                + [(n, ctypes.c_int32) for n in ("axes", "positions_fp32", "pairs", "ladder",
+                                                 "norm")]
+                + [("eps", ctypes.c_float)])
+
+
+_ROTARY = struct.Struct("@7P12qd4i5if")
+assert _ROTARY.size == ctypes.sizeof(Rotary)
+
+
+class Attn(ctypes.Structure):
+    """struct lynx_attn (include/lynx.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in
+                 ("q", "k", "v", "prefix_k", "prefix_v", "cu_q", "cu_k", "out", "lse")]
+                + [(n, ctypes.c_int64) for n in
+                   ("batch", "tokens_q", "tokens_k", "prefix_tokens", "heads", "kv_heads",
+                    "head_dim", "q_batch_stride", "q_stride", "q_head_stride", "k_batch_stride",
+                    "k_stride", "k_head_stride", "v_batch_stride", "v_stride", "v_head_stride",
+                    "out_batch_stride", "out_stride", "out_head_stride", "prefix_k_stride",
+                    "prefix_k_head_stride", "prefix_v_stride", "prefix_v_head_stride")]
+                + [("scale", ctypes.c_float), ("causal", ctypes.c_int32)])
+
+
+_ATTN = struct.Struct("@9P23qfi")
+assert _ATTN.size == ctypes.sizeof(Attn)
+
+
 # every symbol the public headers declare, with (restype, argtypes)
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _LP = ctypes.POINTER(Layer)
@@ -75,6 +114,9 @@ SIGNATURES = {
     "lynx_linear_fp8": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     "lynx_linear_fp8_packed": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     "lynx_block_norm": (_I, [_P, _P]),
+    "lynx_qk_rotary": (_I, [_P, _P]),
+    "lynx_attention_workspace_bytes": (_SZ, [_P]),
+    "lynx_attention": (_I, [_P, _P, _SZ, _P]),
     "lynx_probe_mfma": (_I, [_I, _I, _P, _P, _P, _P, _P]),
     "lynx_probe_mfma_rate": (_I, [_I, _I, _I, _P, _P, _P]),
 }
@@ -546,6 +588,181 @@ def residual_norm(x, y, gate=None, post_norm=None, post_weight=None, post_bias=N
         raise ValueError("residual_norm needs y; use norm_modulate without a branch")
     return _block_norm(x, y, gate, post_norm, post_weight, post_bias, post_eps, residual_scale,
                        norm, weight, bias, scale, shift, eps, fp8, x_out, out)
+
+
+# ---- rotary positions and attention ---------------------------------------------
+
+def _heads(t, shape, dev, name):
+    """(data pointer, token stride, head stride) of a bf16 device tensor [tokens, heads,
+    head_dim] with contiguous channels."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got one on {t.device}")
+    stride = t.stride()
+    if stride[-1] != 1:
+        raise ValueError(f"{name}: its channels must be contiguous")
+    tokens, heads, D = shape[-3:]
+    # the stride of a dimension of one element says nothing
+    return (t.data_ptr(), stride[-3] if tokens > 1 else heads * D,
+            stride[-2] if heads > 1 else D)
+
+
+def _on_device(t, name, dims):
+    if t.dim() not in dims:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dims))} dimensions, got shape "
+                         f"{tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    return t.device
+
+
+def qk_rotary(q, k, positions, axes, theta=10000.0, pairs="adjacent", ladder="axis", norm=None,
+              q_weight=None, k_weight=None, eps=1e-6, out=None):
+    """Rotary positions on several axes for q and k, with the norm of each head before
+    (lynx_qk_rotary).
+
+    q [tokens, heads, head_dim] and k [tokens, kv_heads, head_dim] (or None) bf16, tokens and
+    heads any multiple of 8 elements apart, as in slices of a projection's output; positions
+    [tokens, len(axes)] int32 or float32; axes: how many channels each axis turns.  pairs
+    "adjacent" (channels 2 i, 2 i + 1) or "halves" (i, i + sum(axes) / 2); ladder "axis"
+    (frequencies of each axis' own) or "joint" (one row of them over all axes).  norm "rms"
+    or None, with optional weights [head_dim].  Returns (q', k').  out: the pair of tensors to
+    write, which may be (q, k).
+    """
+    dev = _on_device(q, "q", (3,))
+    T, H, D = q.shape
+    n = len(axes)
+    if not 1 <= n <= 4:
+        raise ValueError(f"axes: 1 to 4 of them, got {n}")
+    if pairs not in PAIR_KINDS or ladder not in LADDER_KINDS or norm not in NORM_KINDS:
+        raise ValueError(f"pairs is one of {list(PAIR_KINDS)}, ladder of {list(LADDER_KINDS)}, "
+                         f"norm None or 'rms'")
+    qp, qt, qh = _heads(q, q.shape, dev, "q")
+    f32 = positions.dtype is torch.float32
+    pos = _expect(positions, torch.float32 if f32 else torch.int32, (T, n), dev, "positions")
+    if out is None:
+        q_out = torch.empty(T, H, D, dtype=torch.bfloat16, device=dev)
+        k_out = None
+        qo, qot, qoh = q_out.data_ptr(), H * D, D
+    else:
+        q_out, k_out = out
+        qo, qot, qoh = _heads(q_out, q.shape, dev, "q_out")
+    kv = kp = kt = kh = ko = kot = koh = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError(f"k: expected 3 dimensions, got shape {tuple(k.shape)}")
+        kv = k.shape[1]
+        kp, kt, kh = _heads(k, (T, kv, D), dev, "k")
+        if out is None:
+            k_out = torch.empty(T, kv, D, dtype=torch.bfloat16, device=dev)
+            ko, kot, koh = k_out.data_ptr(), kv * D, D
+        else:
+            ko, kot, koh = _heads(k_out, k.shape, dev, "k_out")
+    elif k_out is not None:
+        raise ValueError("out: without k there is no second output")
+    a = _ROTARY.pack(
+        qp, kp, 0 if q_weight is None else _expect(q_weight, torch.bfloat16, (D,), dev, "q_weight"),
+        0 if k_weight is None else _expect(k_weight, torch.bfloat16, (D,), dev, "k_weight"),
+        pos, qo, ko, T, H, kv, D, qt, qh, kt, kh, qot, qoh, kot, koh, theta, *axes,
+        *(0,) * (4 - n), n, f32, PAIR_KINDS[pairs], LADDER_KINDS[ladder], NORM_KINDS[norm], eps)
+    _call("lynx_qk_rotary", dev, a)
+    return q_out, k_out
+
+
+def attention_workspace_bytes(batch, tokens_q, tokens_k, heads, kv_heads, head_dim,
+                              prefix_tokens=0, packed=False) -> int:
+    """lynx_attention_workspace_bytes; tokens over all sequences, packed: with offsets."""
+    cu = 4 if packed else 0
+    return lib().lynx_attention_workspace_bytes(
+        _ATTN.pack(0, 0, 0, 0, 0, cu, cu, 0, 0, batch, tokens_q, tokens_k, prefix_tokens, heads,
+                   kv_heads, head_dim, *(0,) * 16, 1.0, 0))
+
+
+def attention(q, k, v, cu_q=None, cu_k=None, causal=False, scale=None, prefix=None,
+              return_lse=False, out=None, lse=None, workspace=None):
+    """out = softmax(scale q k^T) v for a batch of sequences (lynx_attention).
+
+    Packed sequences: q [tokens, heads, head_dim], k and v [tokens, kv_heads, head_dim] bf16
+    with cu_q and cu_k [batch + 1] int32, the sequences' first tokens and the end (cu_k None:
+    cu_q).  Equal lengths: 4-D tensors [batch, tokens, heads, head_dim], or 3-D ones without
+    offsets for one sequence.  Tokens, heads and sequences may be any multiple of 8 elements
+    apart.  causal: query i of Lq sees the keys j <= i + Lk - Lq.  scale: default
+    head_dim ** -0.5.  prefix: (k, v) [tokens, kv_heads, head_dim] that every query sees
+    before its own keys.  Returns out as q, or (out, lse) with lse [tokens, heads] (4-D: [batch,
+    tokens, heads]) float32 where return_lse or lse is given.  out, lse, workspace: the tensors
+    to write.
+    """
+    dev = _on_device(q, "q", (3, 4))
+    shape, bf16 = q.shape, torch.bfloat16
+    dims = len(shape)
+    H, D = shape[-2], shape[-1]
+    if k.dim() != dims:
+        raise ValueError(f"k: expected {dims} dimensions, got shape {tuple(k.shape)}")
+    kv = k.shape[-2]
+    if dims == 4:
+        if cu_q is not None or cu_k is not None:
+            raise ValueError("offsets go with packed 3-D tensors")
+        B, Lq, Lk = shape[0], shape[1], k.shape[1]
+        kshape = (B, Lk, kv, D)
+        Tq, Tk = B * Lq, B * Lk
+        qb, kb, vb = (q.stride(0), k.stride(0), v.stride(0)) if B > 1 else (0, 0, 0)
+        ob = Lq * H * D
+        cq = ck = 0
+    else:
+        Tq, Tk = shape[0], k.shape[0]
+        kshape = (Tk, kv, D)
+        qb = kb = vb = ob = cq = ck = 0
+        B = 1
+        if cu_q is not None:
+            if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+                raise ValueError(f"cu_q: expected shape (batch + 1,), got {tuple(cu_q.shape)}")
+            B = cu_q.shape[0] - 1
+            cq = ck = _expect(cu_q, torch.int32, (B + 1,), dev, "cu_q")
+            if cu_k is not None:
+                ck = _expect(cu_k, torch.int32, (B + 1,), dev, "cu_k")
+            elif Tk != Tq:
+                raise ValueError("cu_k: needed where k has other tokens than q")
+        elif cu_k is not None:
+            raise ValueError("cu_q: needed with cu_k")
+    qp, qt, qh = _heads(q, shape, dev, "q")
+    kp, kt, kh = _heads(k, kshape, dev, "k")
+    vp, vt, vh = _heads(v, kshape, dev, "v")
+    P = pk = pv = pkt = pkh = pvt = pvh = 0
+    if prefix is not None:
+        P = prefix[0].shape[0]
+        pk, pkt, pkh = _heads(prefix[0], (P, kv, D), dev, "prefix k")
+        pv, pvt, pvh = _heads(prefix[1], (P, kv, D), dev, "prefix v")
+        if P == 0:
+            pk = pv = 0
+    if out is None:
+        out = torch.empty(shape, dtype=bf16, device=dev)
+        op, ot, oh = out.data_ptr(), H * D, D
+    else:
+        op, ot, oh = _heads(out, shape, dev, "out")
+        if dims == 4 and B > 1:
+            ob = out.stride(0)
+    if lse is not None:
+        lp = _expect(lse, torch.float32, shape[:-1], dev, "lse")
+    elif return_lse:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    else:
+        lp = 0
+    a = _ATTN.pack(qp, kp, vp, pk, pv, cq, ck, op, lp, B, Tq, Tk, P, H, kv, D, qb, qt, qh, kb, kt,
+                   kh, vb, vt, vh, ob, ot, oh, pkt, pkh, pvt, pvh,
+                   D ** -0.5 if scale is None else scale, bool(causal))
+    if workspace is None:
+        nbytes = lib().lynx_attention_workspace_bytes(a)
+        if nbytes > 0:
+            workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be a contiguous tensor on {dev}")
+    _call("lynx_attention", dev, a, _ptr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out if lse is None else (out, lse)
 
 
 # dense-equivalent flops of one instruction of each probe kind: smfmac

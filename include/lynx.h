@@ -1,6 +1,8 @@
 /*
  * lynx.h - C ABI of the RT-Lynx sparse + LoRA linear layer for AMD MI355X (gfx950),
- * its dense and 8-bit alternatives, and the norms that stand between such layers.
+ * its dense and 8-bit alternatives, the norms that stand between such layers, and
+ * what stands between the QKV and the output projection of a block: rotary positions
+ * and attention.
  *
  * The layer (RT-Lynx page, aitrends.kr, "RT-Lynx: Diffusion Transformers에서
  * GEMM Sparsity를 Activation으로 옮겨 실현하는 방법"; section 방법론, item
@@ -351,6 +353,138 @@ typedef struct lynx_norm {
 } lynx_norm;
 
 lynx_status lynx_block_norm(const lynx_norm* norm, lynx_stream_t stream);
+
+/*
+ * ---- rotary positions -------------------------------------------------------
+ * q and k between their projection and attention, in one pass: the optional rms norm
+ * of each head, then a turn of pairs of channels by the token's positions on up to
+ * four axes (time, height, width, ...):
+ *   x <- x / sqrt(mean(x^2) + eps) * weight      norm LYNX_NORM_RMS, over the D
+ *                                                channels of a head; weight NULL: 1
+ *   (x_m, x_n) <- (x_m cos a - x_n sin a, x_m sin a + x_n cos a)
+ * Axis i turns axis_dims[i] channels; R is their sum.  The R / 2 pairs go to the axes
+ * in order; pair p, the j-th of its axis i, turns by
+ *   a = positions[t][i] * theta^(-2 j / axis_dims[i])   LYNX_LADDER_AXIS: every axis
+ *                                                       has frequencies of its own;
+ *   a = positions[t][i] * theta^(-2 p / R)              LYNX_LADDER_JOINT: the axes
+ *                                                       share one row of frequencies.
+ * Pair p is channels 2 p and 2 p + 1 (LYNX_PAIRS_ADJACENT), or p and p + R / 2
+ * (LYNX_PAIRS_HALVES).  Channels from R on are normed but not turned.
+ * Angles are taken in 64 bits and reduced to one turn before they are rounded, so that
+ * they are as exact far from the start as near it; norm and turn are fp32, and there is
+ * one rounding to bf16.
+ *   - The turn is undone (the backward pass of a turn without a norm) by the same call
+ *     with negated positions.
+ *   - Strides are in elements, between tokens and between heads, multiples of 8, and
+ *     not negative; channels are contiguous.  So q and k may be slices of one
+ *     projection's output.
+ *   - q_out may be q and k_out k, with the same strides; else no output may overlap an
+ *     input, and no two rows of outputs may overlap.
+ *   - A head whose row holds a NaN or an infinity, or whose squares pass fp32's range,
+ *     becomes NaN throughout under a norm.  Without one, NaN and infinities reach their
+ *     pair alone.  A position that is not finite makes its axis' pairs NaN.
+ * Limits: head_dim a multiple of 8, 8..256; 1 to 4 axes, each of an even number >= 2
+ * of channels, R <= head_dim; theta > 0 and finite; 0 <= tokens <= 2^24 (0 is a no-op);
+ * 1 <= q_heads, 0 <= k_heads (0: k, k_out and k_weight are NULL), each <= 1024; tokens *
+ * (q_heads + k_heads) < 2^31; eps >= 0.  Pointers are 16-byte aligned.
+ */
+typedef enum lynx_pairs { LYNX_PAIRS_ADJACENT = 0, LYNX_PAIRS_HALVES = 1 } lynx_pairs;
+typedef enum lynx_ladder { LYNX_LADDER_AXIS = 0, LYNX_LADDER_JOINT = 1 } lynx_ladder;
+
+typedef struct lynx_rotary {
+    const uint16_t* q;        /* tokens x q_heads rows of head_dim bf16 */
+    const uint16_t* k;        /* tokens x k_heads rows, or NULL */
+    const uint16_t* q_weight; /* [head_dim] bf16 or NULL; NULL if norm is NONE */
+    const uint16_t* k_weight; /* [head_dim] bf16 or NULL; NULL if norm is NONE */
+    const void* positions;    /* [tokens][axes] int32, or fp32 */
+    uint16_t* q_out;
+    uint16_t* k_out;
+    int64_t tokens, q_heads, k_heads, head_dim;
+    int64_t q_stride, q_head_stride, k_stride, k_head_stride;
+    int64_t q_out_stride, q_out_head_stride, k_out_stride, k_out_head_stride;
+    double theta;
+    int32_t axis_dims[4];     /* places from `axes` on are not read */
+    int32_t axes;
+    int32_t positions_fp32;   /* 0: int32 */
+    int32_t pairs, ladder;    /* lynx_pairs, lynx_ladder */
+    int32_t norm;             /* LYNX_NORM_NONE or LYNX_NORM_RMS */
+    float eps;
+} lynx_rotary;
+
+lynx_status lynx_qk_rotary(const lynx_rotary* rotary, lynx_stream_t stream);
+
+/*
+ * ---- attention --------------------------------------------------------------
+ * For every query row (token and head) over the keys that it sees:
+ *   out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q . k_j)
+ *   lse = log(sum_j p_j)               natural logarithm, fp32, if lse is given
+ * q has `heads` heads, k and v `kv_heads`; head h reads key head h / (heads / kv_heads).
+ * A call works on `batch` sequences, given in one of two ways:
+ *   packed   cu_q, cu_k (device, batch + 1 int32 each): sequence s has the query tokens
+ *            cu_q[s] .. cu_q[s+1] - 1 and the key tokens cu_k[s] .. cu_k[s+1] - 1, any
+ *            number of either, also none.  The *_batch_stride are not used.
+ *   uniform  cu_q and cu_k NULL: every sequence has tokens_q / batch query tokens and
+ *            tokens_k / batch key tokens, sequences *_batch_stride apart.
+ * A sequence's query i of Lq sees all of its Lk keys or, with `causal`, the keys
+ * j <= i + Lk - Lq (the last query sees every key: single tokens on a cache that
+ * already holds their own keys).  With a prefix (prefix_tokens > 0), every query of every
+ * sequence also sees all prefix keys, which come before the sequence's own; causal
+ * concerns own keys alone.  A query that sees no key gets out = 0 and lse = -infinity.
+ *   - Scores and sums are fp32.  p_j is rounded to bf16 for its product with v_j (not
+ *     for the sum), taken relative to a power of two no further than 2^9 below the
+ *     row's largest; out has one more rounding.  A row's result does not depend on what other
+ *     rows hold, and is the same in every call of the same sizes, offsets and strides.
+ *   - Keys that a query does not see have no influence on it, whatever they hold; with
+ *     NaN or infinities among the keys and values that it sees, its row is as the
+ *     formula gives it (an infinite or NaN value whose p_j is 0 makes NaN), and so with a
+ *     score that passes fp32's range.
+ *   - Rows of out and lse before cu_q[0] and from cu_q[batch] on are left as they were.
+ *     Offsets must not decrease and lie within 0 .. tokens_q (tokens_k); the device checks this only
+ *     so far that no other call's memory is touched: results of other offsets are unspecified.
+ *   - Strides are in elements, multiples of 8, not negative; channels are contiguous.
+ *     Token strides of k, v and the prefix are at least head_dim and below 2^24.  Heads
+ *     may share memory (head stride 0) in inputs.  out overlaps no input, and its rows
+ *     do not overlap.
+ *   - Sequences of any length may be mixed.  Which kernel runs, and whether keys are
+ *     split over workgroups and joined, follows from the totals, so calls whose sequences
+ *     are alike in length are the fastest.
+ * Limits: head_dim a multiple of 8, 8..128; 1 <= kv_heads, heads a multiple of it, <= 1024;
+ * 1 <= batch <= 2^16; tokens_q, tokens_k and prefix_tokens each 0..2^26 (tokens_q == 0
+ * is a no-op), in the uniform form multiples of batch; tokens_q * heads < 2^30; scale > 0
+ * and finite.  q, k, v, out and prefix pointers are 16-byte aligned, cu_* and lse 4-byte.  k and v may be NULL
+ * if tokens_k is 0.
+ */
+typedef struct lynx_attn {
+    const uint16_t* q;        /* bf16 */
+    const uint16_t* k;
+    const uint16_t* v;
+    const uint16_t* prefix_k; /* prefix_tokens x kv_heads rows of head_dim, or NULL */
+    const uint16_t* prefix_v;
+    const int32_t* cu_q;      /* both, or neither */
+    const int32_t* cu_k;
+    uint16_t* out;            /* tokens_q x heads rows of head_dim */
+    float* lse;               /* [tokens_q][heads], or NULL */
+    int64_t batch, tokens_q, tokens_k, prefix_tokens;
+    int64_t heads, kv_heads, head_dim;
+    int64_t q_batch_stride, q_stride, q_head_stride;
+    int64_t k_batch_stride, k_stride, k_head_stride;
+    int64_t v_batch_stride, v_stride, v_head_stride;
+    int64_t out_batch_stride, out_stride, out_head_stride;
+    int64_t prefix_k_stride, prefix_k_head_stride, prefix_v_stride, prefix_v_head_stride;
+    float scale;
+    int32_t causal;
+} lynx_attn;
+
+/*
+ * Bytes of device workspace lynx_attention needs for these sizes (pointers and strides
+ * are not looked at, except whether prefix_tokens is 0); 0 where it needs none, and for
+ * invalid sizes.  Contents on entry irrelevant, clobbered; 256-byte aligned; NULL is
+ * allowed where it is 0.  Calls that may overlap need workspaces of their own.
+ */
+size_t lynx_attention_workspace_bytes(const lynx_attn* attn);
+
+lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t workspace_bytes,
+                           lynx_stream_t stream);
 
 #ifdef __cplusplus
 }
