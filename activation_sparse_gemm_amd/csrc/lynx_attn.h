@@ -16,6 +16,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
+constexpr int kMaxChunks = 128;  // of a pass
+
 // Arguments of an attention kernel.  Query rows of one sequence and key head are numbered
 // token * group + head in group, so that the heads that share a key head share its tiles.
 //
@@ -86,105 +88,99 @@ struct AttnPlan {
     }
 };
 
-// Walks the work of one workgroup.  Workgroups of one XCD (their number mod 8) take the
-// same key heads, one after the other, so that its L2 holds the keys and values that its
-// workgroups read; where there are fewer key heads than XCDs several share a head.  Within a
-// head sequences follow one another, and a sequence's row tiles come last tile first: under a
-// causal mask these have the most keys, and the light ones fill the end.
+// The piece of work of this workgroup; false if there is none.  Uniform over the workgroup.
+// Workgroups of one XCD (their number mod 8) take the same key heads, one after the other, so that
+// its L2 holds the keys and values that its workgroups read; where there are fewer key heads than
+// XCDs several share a head.  Within a head sequences follow one another, and a sequence's row tiles
+// come last tile first: under a causal mask these have the most keys, and the light ones fill the
+// end.
 template <int BM, int BN>
-struct AttnWork {
-    int idx, step, per_head, heads;
-    const AttnArgs& A;
-    int lane;
-
-    __device__ __forceinline__ void range(int s, int& q0, int& lq, int& k0, int& lk) const {
-        const int qa = clampi(A.cu_q[s], 0, A.tokens_q), qb = clampi(A.cu_q[s + 1], qa, A.tokens_q);
-        const int ka = clampi(A.cu_k[s], 0, A.tokens_k), kb = clampi(A.cu_k[s + 1], ka, A.tokens_k);
-        q0 = qa;
-        lq = qb - qa;
-        k0 = ka;
-        lk = kb - ka;
-    }
-    __device__ __forceinline__ int count(int s) const {
-        if (s >= A.batch) return 0;
+__device__ __forceinline__ bool attn_item(const AttnArgs& A, AttnItem& w) {
+    const int lane = threadIdx.x & 63;
+    // of sequence s: its range of tokens, and how many pieces it has to a key head
+    struct Range {
         int q0, lq, k0, lk;
-        range(s, q0, lq, k0, lk);
-        const AttnPlan<BM, BN> p(A, lq, lk);
+    };
+    auto range = [&](int s) {
+        Range r;
+        r.q0 = clampi(A.cu_q[s], 0, A.tokens_q);
+        r.lq = clampi(A.cu_q[s + 1], r.q0, A.tokens_q) - r.q0;
+        r.k0 = clampi(A.cu_k[s], 0, A.tokens_k);
+        r.lk = clampi(A.cu_k[s + 1], r.k0, A.tokens_k) - r.k0;
+        return r;
+    };
+    auto pieces = [&](const Range& r) {
+        const AttnPlan<BM, BN> p(A, r.lq, r.lk);
         return p.tiles * p.chunks;
-    }
-
-    __device__ __forceinline__ explicit AttnWork(const AttnArgs& a) : A(a) {
-        lane = threadIdx.x & 63;
-        if (A.cu_q) {
+    };
+    Range mine = {0, A.len_q, 0, A.len_k};
+    int per_head, sum = 0;  // pieces to a key head; of the sequences up to this lane's (the first 64)
+    if (A.cu_q) {
+        if (lane < A.batch) {
+            mine = range(lane);
+            sum = pieces(mine);
+        }
+        sum = wave_scan(sum, lane);
+        per_head = __builtin_amdgcn_readlane(sum, 63);
+        if (A.batch > 64) {
             int n = 0;
-            for (int s = lane; s < A.batch; s += 64) n += count(s);
-            per_head = __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
-        } else {
-            const AttnPlan<BM, BN> p(A, A.len_q, A.len_k);
-            per_head = A.batch * p.tiles * p.chunks;
+            for (int s = 64 + lane; s < A.batch; s += 64) n += pieces(range(s));
+            per_head += __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
         }
-        const int xcd = int(blockIdx.x) & 7, slot = int(blockIdx.x) >> 3, share = 8 / A.classes;
-        idx = slot * share + xcd / A.classes;
-        step = (int(gridDim.x) >> 3) * share;  // the grid is a multiple of 8
-        heads = A.kv_heads / A.classes;
+    } else {
+        per_head = sgpr(A.batch * pieces(mine));
     }
-
-    // the next piece; false at the end.  Uniform over the workgroup.
-    __device__ __forceinline__ bool next(AttnItem& w) {
-        if (per_head == 0) return false;
-        const int hi = sgpr(idx / per_head);
-        if (hi >= heads) return false;
-        int r = idx - hi * per_head;
-        idx += step;
-        w.kvh = (int(blockIdx.x) & 7) % A.classes + A.classes * hi;
-        if (A.cu_q) {
-            int before = 0, s = 0;
-            for (int base = 0; base < A.batch; base += 64) {
-                const int n = count(base + lane);
-                const int sum = wave_scan(n, lane);
-                const uint64_t over = __ballot(before + sum > r);
-                if (over) {
-                    const int l = __builtin_ctzll(over);
-                    s = base + l;
-                    before += __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(n, l);
-                    break;
-                }
-                before += __builtin_amdgcn_readlane(sum, 63);
+    if (per_head == 0) return false;
+    const int xcd = int(blockIdx.x) & 7, slot = int(blockIdx.x) >> 3, share = 8 / A.classes;
+    const int idx = slot * share + xcd / A.classes, hi = sgpr(idx / per_head);
+    if (hi >= A.kv_heads / A.classes) return false;
+    w.kvh = sgpr(xcd % A.classes + A.classes * hi);
+    int r = idx - hi * per_head;
+    if (A.cu_q) {
+        int before = 0, base = 0;  // pieces before lane 0's sequence, and that sequence
+        uint64_t over = __ballot(sum > r);
+        while (over == 0) {
+            before += __builtin_amdgcn_readlane(sum, 63);
+            base += 64;
+            if (base >= A.batch) return false;  // (the offsets have changed meanwhile)
+            sum = 0;
+            if (base + lane < A.batch) {
+                mine = range(base + lane);
+                sum = pieces(mine);
             }
-            r = sgpr(r - before);
-            w.seq = sgpr(s);
-            int q0, lq, k0, lk;
-            range(w.seq, q0, lq, k0, lk);
-            w.q0 = sgpr(q0);
-            w.lq = sgpr(lq);
-            w.k0 = sgpr(k0);
-            w.lk = sgpr(lk);
-            const AttnPlan<BM, BN> p(A, w.lq, w.lk);
-            w.chunks = p.chunks;
-            w.chunk = sgpr(r / p.tiles);
-            w.tile = p.tiles - 1 - (r - w.chunk * p.tiles);
-        } else {
-            const AttnPlan<BM, BN> p(A, A.len_q, A.len_k);
-            const int per = p.tiles * p.chunks;
-            const int s = sgpr(r / per);
-            r -= s * per;
-            w.seq = s;
-            w.q0 = s * A.len_q;
-            w.lq = A.len_q;
-            w.k0 = int64_t(s) * A.len_k;
-            w.lk = A.len_k;
-            w.chunks = p.chunks;
-            w.chunk = sgpr(r / p.tiles);
-            w.tile = p.tiles - 1 - (r - w.chunk * p.tiles);
+            sum = wave_scan(sum, lane);
+            over = __ballot(before + sum > r);
         }
-        return true;
+        const int l = __builtin_ctzll(over);
+        if (l > 0) before += __builtin_amdgcn_readlane(sum, l - 1);
+        r = sgpr(r - before);
+        w.seq = base + l;
+        w.q0 = __builtin_amdgcn_readlane(mine.q0, l);
+        w.lq = __builtin_amdgcn_readlane(mine.lq, l);
+        w.k0 = __builtin_amdgcn_readlane(mine.k0, l);
+        w.lk = __builtin_amdgcn_readlane(mine.lk, l);
+    } else {
+        const int per = sgpr(pieces(mine));
+        w.seq = sgpr(r / per);
+        r -= w.seq * per;
+        w.q0 = w.seq * A.len_q;
+        w.lq = A.len_q;
+        w.k0 = 0;
+        w.lk = A.len_k;
     }
-};
+    const AttnPlan<BM, BN> p(A, w.lq, w.lk);
+    const int tiles = sgpr(p.tiles);
+    w.chunks = sgpr(p.chunks);
+    w.chunk = sgpr(r / tiles);
+    w.tile = tiles - 1 - (r - w.chunk * tiles);
+    return true;
+}
 
 // ---- launchers --------------------------------------------------------------
 lynx_status launch_qk_rotary(const lynx_rotary& d, hipStream_t stream);
 
 lynx_status launch_attn_tile(const AttnArgs& a, int grid, hipStream_t stream);
+lynx_status launch_attn_wide(const AttnArgs& a, int grid, hipStream_t stream);
 lynx_status launch_attn_few(const AttnArgs& a, int grid, hipStream_t stream);
 lynx_status launch_attn_join(const AttnArgs& a, int prefix_slots, hipStream_t stream);
 

@@ -1,5 +1,6 @@
 // C ABI of rotary positions and attention: argument validation, the choice of kernel and of
 // the split of keys, workspace layout and dispatch.  Defined in lynx.h.
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 #include <numeric>
@@ -103,8 +104,9 @@ lynx_status validate_attn(const lynx_attn& d, bool* noop) {
 }
 
 // One launch over keys: which kernel, and how keys are cut.
+enum class Kernel { few, tile, wide };
 struct Pass {
-    bool few;
+    Kernel kernel;
     int chunk_tiles, chunk_max;  // as in AttnArgs; chunk_max 1: not cut
     int64_t grid;
 };
@@ -118,50 +120,101 @@ struct Plan {
 
 constexpr int kUnits = 256;
 
-// rows: query rows to a key head, over all sequences; keys: of all sequences together, shared:
-// keys that each sequence has besides
-Pass plan_pass(int64_t batch, int64_t rows, int64_t keys, int64_t shared, int64_t kv_heads, bool ragged) {
-    Pass p;
-    const int64_t mean_rows = (rows + batch - 1) / batch;
-    p.few = mean_rows <= 32;
-    const int64_t bm = p.few ? 32 : 128, bn = p.few ? 128 : 64;
-    const int64_t tiles = batch * ((mean_rows + bm - 1) / bm) * kv_heads;     // of rows, about
-    const int64_t kt = ((keys + batch - 1) / batch + shared + bn - 1) / bn;   // key tiles of one
-    const int64_t want = p.few ? 2 * kUnits : 2 * kUnits;
-    int64_t chunks = tiles >= want ? 1 : want / tiles;
-    const int64_t least = p.few ? 2 : 4;
-    chunks = std::max<int64_t>(1, std::min(chunks, kt / least));
-    int64_t per = std::max<int64_t>(1, (kt + chunks - 1) / chunks);
-    // sequences longer than the mean have more chunks
-    const int64_t all = (keys + shared + bn - 1) / bn;
-    int64_t top = ragged ? (all + per - 1) / per : (kt + per - 1) / per;
-    if (ragged && p.few && top > 1) {
-        // one long sequence among short ones is cut too
-    } else if (chunks == 1) {
-        top = 1;
+// Which kernel takes a pass, and into how many chunks it cuts the keys.  rows: query rows to a
+// key head, over all sequences; keys: of all sequences together; shared: keys that each sequence has
+// besides; seen: the share of the keys that a mask leaves; joined: whether the join runs anyway.
+Pass plan_pass(int64_t batch, int64_t rows, int64_t keys, int64_t shared, int64_t kv_heads, int64_t D,
+               bool ragged, double seen, bool joined) {
+    Pass p = {};
+    constexpr int64_t kMaxPartial = int64_t(1) << 28;
+    const int64_t mean_rows = (rows + batch - 1) / batch, row_bytes = kv_heads * rows * (D * 4 + 16);
+    auto tiles_of = [&](int64_t m) { return batch * ((mean_rows + m - 1) / m) * kv_heads; };
+    // per: key tiles of a chunk; top: the most chunks of a sequence, and no more than 256 MB of
+    // partial results for the sake of uneven lengths
+    auto finish = [&](Kernel kernel, int64_t bm, int64_t bn, int64_t per, int64_t chunks) {
+        const int64_t most = (keys + bn - 1) / bn + (shared + bn - 1) / bn;  // were all in one sequence
+        int64_t top = ragged && chunks > 0 ? (most + per - 1) / per : chunks;
+        top = std::min(top, std::max(chunks, kMaxPartial / row_bytes));
+        top = std::max<int64_t>(1, std::min<int64_t>(top, kMaxChunks));
+        p.kernel = kernel;
+        p.chunk_tiles = int(per);
+        p.chunk_max = int(top);
+        // The length of the work list, at most: a sequence has one row tile, and one more for
+        // every bm rows, and its chunks hold `per` key tiles each but the last one
+        int64_t items = tiles_of(bm) / kv_heads * top;
+        if (ragged) {
+            const int64_t all = keys / bn + batch * (1 + (shared + bn - 1) / bn);
+            items = (rows / bm + batch) * top;
+            items = std::min(items, all / per + batch + rows / bm * top);
+        }
+        const int64_t classes = std::gcd<int64_t>(kv_heads, 8), share = 8 / classes;
+        p.grid = 8 * ((kv_heads / classes * items + share - 1) / share);
+    };
+    if (mean_rows <= 32) {
+        // Bound by the keys' bytes: two workgroups to a unit, and no fewer than that.  Sequences
+        // of different lengths are cut into four times as many chunks of one size, so that the
+        // units end together: 32 tokens on caches of 17 .. 16400 keys 212 us, without 229.
+        const int64_t kt = std::max<int64_t>(1, ((keys + batch - 1) / batch + shared + 127) / 128);
+        const int64_t tiles = tiles_of(32), want = (ragged && batch > 1 ? 8 : 2) * kUnits;
+        // (at least 4 tiles, 8 with all 32 rows: partial results are then an eighth of the keys)
+        int64_t per = std::max({int64_t(4), mean_rows / 4, (tiles * kt + want - 1) / want});
+        const int64_t chunks = (kt + per - 1) / per;
+        if (!ragged || batch == 1) per = (kt + chunks - 1) / chunks;
+        finish(Kernel::few, 32, 128, per, chunks);
+        return p;
     }
-    top = std::max<int64_t>(1, std::min<int64_t>(top, 64));
-    // no more than 256 MB of partial results for the sake of uneven lengths
-    top = std::min(top, std::max(chunks, (int64_t(1) << 28) / (rows * kv_heads * 528)));
-    p.chunk_tiles = int(per);
-    p.chunk_max = int(top);
-    const int64_t most_tiles = (ragged ? rows / bm + batch : batch * ((mean_rows + bm - 1) / bm));
-    int64_t items = most_tiles * top;  // to a key head, at most
-    const int64_t classes = std::gcd<int64_t>(kv_heads, 8), share = 8 / classes;
-    int64_t grid = 8 * ((kv_heads / classes * items + share - 1) / share);
-    if (top > 1) grid = std::min<int64_t>(grid, p.few ? kUnits : 2 * kUnits);
-    p.grid = std::min<int64_t>(grid, int64_t(1) << 22);
+    // By estimated time.  A compute unit takes, per tile of keys (128 channels: 64 keys; up to 64
+    // channels: 128):
+    //   128 rows (tile)  1.03 us (1.2), two workgroups to a unit taking as long as one after
+    //                    the other: 16384 x 16384 x 8 heads 1058 us
+    //   256 rows (wide)  1.92 us (2.28), one workgroup to a unit: 985 us
+    // and 5 us for what comes before and after.  Under a causal mask row tiles differ, and units
+    // that have light ones take more of them; but the heaviest takes its time.  Cutting needs
+    // the join: 4 us, and its bytes, which are written and read at 4 TB/s.
+    const int64_t bn = D <= 64 ? 128 : 64;
+    const int64_t kt = ((keys + batch - 1) / batch + shared + bn - 1) / bn;
+    double best = 0.0;
+    // (packed sequences differ: the 256-row tiles of a long one end late)
+    for (int wide = 0; wide < (ragged && batch > 1 ? 1 : 2); ++wide) {
+        const int64_t bm = wide ? 256 : 128, tiles = tiles_of(bm);
+        const double step = wide ? (D <= 64 ? 2.28 : 1.92) : (D <= 64 ? 1.20 : 1.03);
+        for (int64_t chunks = 1; chunks <= kMaxChunks && (chunks == 1 || chunks * 2 <= kt + 1); ++chunks) {
+            const int64_t per = std::max<int64_t>(1, (kt + chunks - 1) / chunks), items = tiles * chunks;
+            if (chunks > 1 && row_bytes * chunks > kMaxPartial) break;
+            double us = double((items + kUnits - 1) / kUnits) * double(per) * step;
+            if (seen < 1.0)
+                us = std::max(double(items) / kUnits * double(per) * seen * step,
+                              double(per) * step * (wide || items <= kUnits ? 1.0 : 1.6));
+            if (joined) us += double(row_bytes * chunks) * 2.0 / 4.0e6;
+            else if (chunks > 1) us += 4.0 + double(row_bytes * chunks) * 2.0 / 4.0e6;
+            if (best == 0.0 || us < best) {
+                best = us;
+                finish(wide ? Kernel::wide : Kernel::tile, bm, bn, per, chunks == 1 ? 0 : chunks);
+            }
+            if (items >= 8 * kUnits) break;
+        }
+    }
     return p;
 }
 
 Plan make_plan(const lynx_attn& d, bool ragged) {
     Plan P = {};
+    if (d.tokens_q == 0) return P;
     const int64_t group = d.heads / d.kv_heads, rows = d.tokens_q * group;
-    P.apart = d.prefix_tokens > 0 && d.batch > 1 && rows / d.batch < 128;
-    P.own = plan_pass(d.batch, rows, d.tokens_k, P.apart ? 0 : d.prefix_tokens, d.kv_heads, ragged);
+    // A prefix is worked on once for all sequences where their rows alone do not fill row tiles
+    // (and where the partial results of both passes are not past a GiB)
+    P.apart = d.prefix_tokens > 0 && d.batch > 1 && rows / d.batch < 128 &&
+              d.tokens_q * d.heads * (d.head_dim * 4 + 16) <= (int64_t(1) << 29);
+    const int64_t shared = P.apart ? 0 : d.prefix_tokens;
+    double seen = 1.0;
+    if (d.causal) {
+        const double keys = double(d.tokens_k) + double(d.batch) * double(shared);
+        if (keys > 0.0) seen = std::max(0.5, 1.0 - 0.5 * double(d.tokens_q) / keys);
+    }
+    P.own = plan_pass(d.batch, rows, d.tokens_k, shared, d.kv_heads, d.head_dim, ragged, seen, P.apart);
     int slots = P.own.chunk_max > 1 ? P.own.chunk_max : 0;
     if (P.apart) {
-        P.prefix = plan_pass(1, rows, d.prefix_tokens, 0, d.kv_heads, false);
+        P.prefix = plan_pass(1, rows, d.prefix_tokens, 0, d.kv_heads, d.head_dim, false, 1.0, true);
         slots = P.own.chunk_max + P.prefix.chunk_max;
     }
     P.slots = slots;
@@ -257,7 +310,11 @@ lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t worksp
     a.causal = d.causal != 0;
 
     auto run = [&](const AttnArgs& args, const Pass& p) {
-        return p.few ? launch_attn_few(args, int(p.grid), s) : launch_attn_tile(args, int(p.grid), s);
+        switch (p.kernel) {
+            case Kernel::few: return launch_attn_few(args, int(p.grid), s);
+            case Kernel::tile: return launch_attn_tile(args, int(p.grid), s);
+            default: return launch_attn_wide(args, int(p.grid), s);
+        }
     };
     if (P.apart) {
         AttnArgs p = a;

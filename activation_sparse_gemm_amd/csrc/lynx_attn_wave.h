@@ -14,6 +14,8 @@
 // chunks that are permuted within the row so that neither read has bank conflicts.
 #pragma once
 
+#include <type_traits>
+
 #include "lynx_attn.h"
 
 namespace lynx {
@@ -28,17 +30,44 @@ __device__ __forceinline__ int swz_v(int r) {
     return DP == 128 ? ((r & 3) << 2 | ((r >> 2) & 3)) : (((r >> 1) & 1) << 2 | ((r >> 2) & 3));
 }
 
-// Stages BN rows of K or V into LDS: waves W0 .. W0 + NW - 1 of the workgroup take 1 KB
-// pieces in turn.  Rows from `rows` on and channels from D on become zero.
-template <int DP, int BN, int NW, bool IS_V>
-struct AttnStage {
-    static constexpr int CH = DP / 8, PIECES = BN * DP * 2 / 1024, PER = PIECES / NW;
-    static_assert(PIECES % NW == 0, "");
-    uint32_t voff[PER];
-    uint32_t tile_bytes;  // from one tile to the next
-    uint32_t stride;      // bytes from one row to the next
+// The keys that an item works on, in tiles of BN: first those of the prefix (tp tiles), then the
+// sequence's own.  Tiles j0 .. j0 + n - 1 are the item's.
+template <int BMR, int BN>
+struct AttnSpan {
+    int tp, j0, n;
+    __device__ __forceinline__ AttnSpan(const AttnArgs& A, const AttnItem& w) {
+        const AttnPlan<BMR, BN> plan(A, w.lq, w.lk);
+        const int per = sgpr(plan.per);
+        // up to the last own key that the last query of the row tile sees
+        const int last = min(w.lq - 1, sgpr((w.tile * BMR + BMR - 1) / A.group));
+        const int own = A.causal ? clampi(last + w.lk - w.lq + 1, 0, w.lk) : w.lk;
+        tp = (A.prefix + BN - 1) / BN;
+        j0 = w.chunk * per;
+        n = max(0, min(j0 + per, tp + (own + BN - 1) / BN) - j0);
+    }
+    // the first key of tile j within its segment, and the first row that is not there
+    __device__ __forceinline__ int key(int j) const { return (j < tp ? j : j - tp) * BN; }
+};
 
-    __device__ __forceinline__ void init(int64_t row_stride, int D, int wave, int lane) {
+// The tiles of K, or of V, of a workgroup (or of one wave of it), one after the other, into a ring
+// in LDS.  A tile is R rows, `span` rows from the one before; NW waves stage it together, 1 KB
+// pieces in turn.  Rows past the item's last tile, and channels from head_dim on, become zero.
+template <int DP, int R, int NW, int RING, bool IS_V>
+struct TileStream {
+    static constexpr int CH = DP / 8, BYTES = R * DP * 2, PER = BYTES / 1024 / NW;
+    static_assert(PER * NW * 1024 == BYTES, "");
+    uint32_t voff[PER];
+    const uint16_t *p, *own;  // the next tile; the sequence's first
+    int64_t own_stride;       // elements from row to row
+    uint32_t stride;          // bytes, of the present segment
+    int span;
+    int rows, own_rows;       // from the next tile's first row to the segment's end
+    int left;                 // tiles of the prefix that are still to come
+    uint32_t lds, slot;
+    i32x4 rs;
+    uint32_t to;
+
+    __device__ __forceinline__ void offsets(int64_t row_stride, int D, int wave, int lane) {
         stride = uint32_t(row_stride) * 2u;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -47,170 +76,235 @@ struct AttnStage {
             voff[i] = 8 * c < D ? uint32_t(row) * stride + 16u * uint32_t(c) : 0x80000000u;
         }
     }
-    // base: the tile's first row; rows: how many of its rows there are (others read zero)
-    __device__ __forceinline__ void load(const uint16_t* base, int rows, int D, uint32_t lds,
-                                         int wave) const {
-        const int n = clampi(rows, 0, BN);
-        i32x4 rs = make_rsrc(base, n > 0 ? uint32_t(n - 1) * stride + 2u * uint32_t(D) : 0u);
+    // base, t: the sequence's keys of this head and their stride; pbase, pt: the prefix'.  first:
+    // the stream's first row within a tile of BN rows.
+    template <int BMR, int BN>
+    __device__ __forceinline__ void open(const AttnSpan<BMR, BN>& span_, int prefix, int lk, const uint16_t* base,
+                                         int64_t t, const uint16_t* pbase, int64_t pt, int first, int D,
+                                         uint32_t lds_, int wave, int lane) {
+        const int end = span_.j0 + span_.n, tp = span_.tp, j0 = span_.j0;
+        span = BN;
+        lds = lds_ + uint32_t(wave * PER) * 1024u;
+        slot = 0;
+        own = base + first * t;
+        own_rows = min(lk, max(end - tp, 0) * BN) - first;
+        own_stride = t;
+        if (j0 < tp) {
+            p = pbase + (int64_t(j0) * BN + first) * pt;
+            rows = min(prefix, end * BN) - j0 * BN - first;
+            left = tp - j0;
+            offsets(pt, D, wave, lane);
+        } else {
+            p = own + int64_t(j0 - tp) * BN * t;
+            rows = own_rows - (j0 - tp) * BN;
+            left = -1;
+            offsets(t, D, wave, lane);
+        }
+    }
+    // The next tile's loads: begin, then each of PER pieces.
+    __device__ __forceinline__ void begin(int D, int wave, int lane) {
+        if (left == 0) {
+            p = own;
+            rows = own_rows;
+            offsets(own_stride, D, wave, lane);
+        }
+        --left;
+        const int n = min(rows, R);
+        rs = make_rsrc(p, n > 0 ? uint32_t(n - 1) * stride + 2u * uint32_t(D) : 0u);
         rs = i32x4{sgpr(rs[0]), sgpr(rs[1]), sgpr(rs[2]), rs[3]};
+        to = lds + slot;
+        p += (int64_t(stride) * span) >> 1;
+        rows -= span;
+        slot = slot == (RING - 1) * BYTES ? 0 : slot + BYTES;
+    }
+    __device__ __forceinline__ void piece(int i) const {
+        dma16(uint32_t(sgpr(int(to + uint32_t(i) * 1024u))), voff[i], rs, 0);
+    }
+    __device__ __forceinline__ void issue(int D, int wave, int lane) {
+        begin(D, wave, lane);
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            dma16(uint32_t(sgpr(int(lds + uint32_t(wave * PER + i) * 1024u))), voff[i], rs, 0);
+        for (int i = 0; i < PER; ++i) piece(i);
     }
 };
 
-template <int DP, int QB, bool LSE>
+template <int DP, bool LSE>
 struct AttnWave {
     static constexpr int KS = DP / 16, DB = DP / 32;
-    bf16x8 q[QB][KS];
-    f32x16 o[QB][DB];
+    bf16x8 q[KS];
+    f32x16 o[DB];
     // m: a whole power of two, -inf before the first key that is seen; l: the sum of the
     // weights as the product with V takes them, rounded to bf16, so that a row on which one key
     // dominates is not off by that key's rounding; exact: of the weights before it, for lse
-    float m[QB], l[QB], exact[LSE ? QB : 1];
-    uint32_t ka, va;     // LDS offsets of this lane's operands
+    float m, l, exact;
     int lane, h;
 
-    __device__ __forceinline__ void init(int lane_) {
-        lane = lane_;
+    // p: the lane's query row, or NULL
+    __device__ __forceinline__ void init(const uint16_t* p, int D) {
+        lane = threadIdx.x & 63;
         h = lane >> 5;
-        ka = uint32_t(lane & 31);
-        va = 0;
+        m = -INFINITY;
+        l = exact = 0.f;
 #pragma unroll
-        for (int b = 0; b < QB; ++b) {
-            m[b] = -INFINITY;
-            l[b] = 0.f;
-            if constexpr (LSE) exact[b] = 0.f;
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[b][d][e] = 0.f;
-        }
-    }
-
-    // this lane's query of block b; p: its row, or NULL
-    __device__ __forceinline__ void load_q(int b, const uint16_t* p, int D) {
+            for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int d = 16 * s + 8 * h;
             u32x4 v = {};
             if (p && d < D) v = *reinterpret_cast<const u32x4*>(p + d);
-            q[b][s] = __builtin_bit_cast(bf16x8, v);
+            q[s] = __builtin_bit_cast(bf16x8, v);
         }
     }
 
-    // S^T of the 32 keys from row `row` of the K tile at LDS byte `lds`
-    __device__ __forceinline__ void scores(const char* smem, uint32_t lds, int row, f32x16 (&s)[QB]) {
-#pragma unroll
-        for (int b = 0; b < QB; ++b)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
+    // Where this lane's operands lie in a tile: of 32 rows of K at channels 16 i .., and of 16
+    // rows of V, u = 0, 1 its rows 0-3 and 8-11 (h = 1: 4-7 and 12-15), at channels 32 db ..  The
+    // permutations are exclusive ors, so the others follow from the first by one instruction.
+    __device__ __forceinline__ uint32_t k_first() const {
         const int r = lane & 31;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            const uint32_t off = uint32_t(r) * (DP * 2) + uint32_t(((2 * i + h) ^ swz_k<DP>(r)) * 16);
-            const bf16x8 k =
-                *reinterpret_cast<const bf16x8*>(smem + lds + uint32_t(row) * (DP * 2) + off);
-#pragma unroll
-            for (int b = 0; b < QB; ++b)
-                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[b][i], s[b], 0, 0, 0);
-        }
+        return uint32_t(r) * (DP * 2) + uint32_t((h ^ swz_k<DP>(r)) * 16);
     }
-
-    // V^T's operand: channels 32 db .., keys row + 16 t ..
-    __device__ __forceinline__ bf16x8 v_operand(const char* smem, uint32_t lds, int row, int db) {
-        const int i = lane & 15, dsub = (lane >> 4) & 1;
-        bf16x4 part[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = 8 * u + 4 * h + (i >> 2);
-            const int c = 4 * db + 2 * dsub + ((i & 3) >> 1);
-            const uint32_t off =
-                uint32_t(r) * (DP * 2) + uint32_t((c ^ swz_v<DP>(r)) * 16 + 8 * (i & 1));
-            part[u] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-                (__attribute__((address_space(3))) bf16x4*)(smem + lds + uint32_t(row) * (DP * 2) + off));
-        }
-        return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    __device__ __forceinline__ static uint32_t k_at(uint32_t first, int i) { return first ^ uint32_t(32 * i); }
+    __device__ __forceinline__ uint32_t v_first() const {
+        const int i = lane & 15, r = 4 * h + (i >> 2), c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+        return uint32_t(r) * (DP * 2) + uint32_t((c ^ swz_v<DP>(r)) * 16 + 8 * (i & 1));
+    }
+    __device__ __forceinline__ static uint32_t v_at(uint32_t first, int u, int db) {
+        return (first ^ uint32_t(64 * db + 32 * u)) + uint32_t(u * 8 * DP * 2);
+    }
+    __device__ __forceinline__ static bf16x8 v_pair(const char* a, const char* b) {
+        const bf16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) bf16x4*)a);
+        const bf16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) bf16x4*)b);
+        return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 
     // Hides keys: those of this lane's query from `seen` on; key0: the block's first key
     __device__ __forceinline__ void mask(f32x16& s, int key0, int seen) const {
+        const int left = seen - key0 - 4 * h;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            if (key0 + 8 * (e / 4) + 4 * h + e % 4 >= seen) s[e] = -INFINITY;
+            if (8 * (e / 4) + e % 4 >= left) s[e] = -INFINITY;
     }
 
     // a row's maximum, or sum, from the two lanes that hold its halves
     __device__ __forceinline__ static float both_max(float v) {
         const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        return __builtin_elementwise_maximum(__uint_as_float(w[0]), __uint_as_float(w[1]));
     }
     __device__ __forceinline__ static float both_sum(float v) {
         const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
         return __uint_as_float(w[0]) + __uint_as_float(w[1]);
     }
 
-    // Scores to weights, in place, for NKB blocks of 32 keys.  p = 2^(c s - m); m is raised,
-    // and what was summed before scaled down, where a row's maximum is 2^8 above it: then l and
-    // o stay in range, and m, a whole number, changes no bits of the sums' fractions.
-    template <int NKB>
-    __device__ __forceinline__ void softmax(int b, f32x16 (&s)[NKB][QB], float c) {
-        float top = s[0][b][0];
-#pragma unroll
-        for (int n = 0; n < NKB; ++n)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][b][e]);
-        top = both_max(top) * c;
-        const bool raise = top > m[b] + 8.f;
-        if (__ballot(raise)) {
-            const float to = raise ? ceilf(top) : m[b];
-            const float f = raise ? __builtin_amdgcn_exp2f(m[b] - to) : 1.f;
-            m[b] = to;
-            l[b] *= f;
-            if constexpr (LSE) exact[b] *= f;
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[b][d][e] *= f;
-        }
-        const float base = m[b] == -INFINITY ? 0.f : m[b];
-#pragma unroll
-        for (int n = 0; n < NKB; ++n)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                s[n][b][e] = __builtin_amdgcn_exp2f(fmaf(s[n][b][e], c, -base));
-                if constexpr (LSE) exact[b] += s[n][b][e];
-            }
-    }
-
-    __device__ __forceinline__ static bf16x8 weights(const f32x16& s, int t, float& l) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        const bf16x2 one = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
-        u32x4 w;
+    // The maximum of a row's scores, times c, in both of its lanes.  (elementwise_maximum keeps a
+    // NaN: its weight is NaN whatever m is, and so is the row.)  Four chains: a chain's step
+    // takes 8 cycles, others 5 (with the matrix unit at work).
+    template <int NB>
+    __device__ __forceinline__ static float maximum(const f32x16 (&s)[NB], float c) {
+        float top[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t p = pack_bf16(s[8 * t + 2 * i], s[8 * t + 2 * i + 1]);
-            l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), one, l, false);
-            w[i] = p;
+            top[i] = s[0][i];
+#pragma unroll
+            for (int e = i + 4; e < 16 * NB; e += 4)
+                top[i] = __builtin_elementwise_maximum(top[i], s[e / 16][e % 16]);
         }
-        return __builtin_bit_cast(bf16x8, w);
+        const float x = __builtin_elementwise_maximum(top[0], top[1]);
+        return both_max(__builtin_elementwise_maximum(__builtin_elementwise_maximum(x, top[2]), top[3])) * c;
     }
 
-    // O^T += V^T P^T over the 32 keys from row `row` of the V tile
-    __device__ __forceinline__ void accumulate(const char* smem, uint32_t lds, int row, const f32x16 (&s)[QB]) {
+    // p = 2^(c s - m).  m is raised to the whole number above a row's maximum, and what was summed
+    // before scaled down, where the maximum is 2^8 above it: then l and o stay in range, and m, a
+    // whole number, changes no bits of the sums' fractions.
+    __device__ __forceinline__ void raise(float top) {
+        const bool up = top > m + 8.f;
+        if (!__ballot(up)) return;
+        const float to = up ? ceilf(top) : m;
+        const float f = up ? __builtin_amdgcn_exp2f(m - to) : 1.f;
+        m = to;
+        l *= f;
+        exact *= f;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            bf16x8 p[QB];
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int b = 0; b < QB; ++b) p[b] = weights(s[b], t, l[b]);
+            for (int e = 0; e < 16; ++e) o[d][e] *= f;
+    }
+
+    // Scores of 32 keys to weights, P^T's operand for two steps of 16 keys, and their sums: two
+    // partial sums to a step, since a chain's step takes longer.
+    __device__ __forceinline__ void weights(f32x16& s, float c, u32x4 (&p)[2], float (&sum)[4]) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 one = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
+        const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const bf16x8 v = v_operand(smem, lds, row + 16 * t, d);
+        for (int e = 0; e < 16; ++e) {
+            s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -base));
+            if constexpr (LSE) exact += s[e];
+        }
 #pragma unroll
-                for (int b = 0; b < QB; ++b)
-                    o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[b], o[b][d], 0, 0, 0);
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = pack_bf16(s[2 * i], s[2 * i + 1]);
+            sum[i % 4] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, sum[i % 4], false);
+            p[i / 4][i % 4] = w;
+        }
+    }
+};
+
+// The products of a wave's 32 rows with tiles of BN keys in LDS: S^T = K Q^T of one tile together
+// with O^T += V^T P^T of the tile before, which leaves neither waiting for itself.  Operands are
+// read AHEAD products early.  k, v: LDS offsets of a tile plus the lane's k_first or v_first.
+template <int DP, int BN, bool LSE>
+struct AttnTile : AttnWave<DP, LSE> {
+    using W = AttnWave<DP, LSE>;
+    static constexpr int NB = BN / 32, NM = NB * W::KS, AHEAD = 4;
+    static_assert(NM == 2 * NB * W::DB, "as many products of either kind");
+    f32x16 s[NB];
+    u32x4 p[NB][2];
+    bf16x8 kf[NM], vf[NM];
+
+    __device__ __forceinline__ void read(const char* smem, uint32_t k, uint32_t v, int i, bool qk, bool pv) {
+        if (qk)
+            kf[i] = *reinterpret_cast<const bf16x8*>(smem + W::k_at(k, i / NB) + (i % NB) * (32 * DP * 2));
+        if (pv) {
+            const char* at = smem + (i / W::DB) * (16 * DP * 2);
+            vf[i] = W::v_pair(at + W::v_at(v, 0, i % W::DB), at + W::v_at(v, 1, i % W::DB));
+        }
+    }
+    template <bool QK, bool PV>
+    __device__ __forceinline__ void ahead(const char* smem, uint32_t k, uint32_t v) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) read(smem, k, v, i, QK, PV);
+    }
+    template <bool QK, bool PV>
+    __device__ __forceinline__ void multiply(const char* smem, uint32_t k, uint32_t v) {
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+            if (i + AHEAD < NM) read(smem, k, v, i + AHEAD, QK, PV);
+            if constexpr (QK) {
+                f32x16 c = s[i % NB];
+                if (i < NB) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) c[e] = 0.f;
+                }
+                s[i % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], W::q[i / NB], c, 0, 0, 0);
+            }
+            if constexpr (PV) {
+                const int t = i / W::DB, d = i % W::DB;
+                W::o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i], __builtin_bit_cast(bf16x8, p[t / 2][t % 2]),
+                                                                 W::o[d], 0, 0, 0);
             }
         }
+        constexpr int reads = (QK ? 1 : 0) + (PV ? 2 : 0), products = (QK ? 1 : 0) + (PV ? 1 : 0);
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+            if (i + AHEAD < NM) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, products, 0);
+        }
+    }
+    // Hides keys from `seen` on; key0: the tile's first
+    __device__ __forceinline__ void hide(int key0, int seen) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) W::mask(s[b], key0 + 32 * b, seen);
     }
 };
 
@@ -230,5 +324,80 @@ __device__ __forceinline__ int64_t attn_o_offset(const AttnArgs& A, int token, i
     const int b = token / A.addr_len;
     return b * A.o_b + (token - b * A.addr_len) * A.o_t + head * A.o_h;
 }
+
+// Writes a wave's rows (row0 ..): to out and lse, or as a chunk's partial result.
+template <int DP, bool LSE>
+__device__ __forceinline__ void store_rows(const AttnArgs& A, const AttnItem& w, const AttnWave<DP, LSE>& W,
+                                           int row0, bool part) {
+    const float l = W.both_sum(W.l), le = LSE ? W.both_sum(W.exact) : 0.f;
+    int token, head;
+    if (!attn_row(A, w, row0 + (W.lane & 31), token, head)) return;
+    const int64_t row = int64_t(token) * A.heads + head;
+    if (part) {
+        const int64_t slot = row * A.slots + A.slot0 + w.chunk;
+        float* o = A.part_o + slot * A.D;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int at = 32 * d + 8 * g + 4 * W.h;
+                if (at < A.D)
+                    *reinterpret_cast<f32x4*>(o + at) =
+                        f32x4{W.o[d][4 * g], W.o[d][4 * g + 1], W.o[d][4 * g + 2], W.o[d][4 * g + 3]};
+            }
+        if (W.h == 0) {
+            A.part_ml[slot] = float4{W.m, l, le, 0.f};
+            if (w.chunk == 0) A.part_n[row] = w.chunks;
+        }
+        return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* o = A.out + attn_o_offset(A, token, head);
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int at = 32 * d + 8 * g + 4 * W.h;
+            if (at < A.D)
+                *reinterpret_cast<u32x2*>(o + at) =
+                    u32x2{pack_bf16(W.o[d][4 * g] * inv, W.o[d][4 * g + 1] * inv),
+                          pack_bf16(W.o[d][4 * g + 2] * inv, W.o[d][4 * g + 3] * inv)};
+        }
+    if (W.h == 0) {
+        if constexpr (LSE) A.lse[row] = le == 0.f ? -INFINITY : (W.m + log2f(le)) * kLn2;
+        if (A.slots > 0 && w.chunk == 0) A.part_n[row] = 1;
+    }
+}
+
+// K's (V's) streams of an item
+template <class S, int BMR, int BN>
+__device__ __forceinline__ void open_stream(S& s, const AttnArgs& A, const AttnItem& w, const AttnSpan<BMR, BN>& span,
+                                            bool v, int first, uint32_t lds, int wave, int lane) {
+    const int64_t t = v ? A.v_t : A.k_t, pt = v ? A.pv_t : A.pk_t;
+    const uint16_t* base = (v ? A.v : A.k) + (A.cu_k ? w.k0 * t : w.seq * (v ? A.v_b : A.k_b)) +
+                           w.kvh * (v ? A.v_h : A.k_h);
+    const uint16_t* pbase = (v ? A.pv : A.pk) + w.kvh * (v ? A.pv_h : A.pk_h);
+    s.open(span, A.prefix, w.lk, base, t, pbase, pt, first, A.D, lds, wave, lane);
+}
+
+// What a wave's rows see of the sequence's own keys: a lane's row `seen`, all of them `all`, any
+// of them `any`.  none: the wave has no row.
+struct AttnView {
+    int seen, all, any;
+    bool none;
+    __device__ __forceinline__ AttnView(const AttnArgs& A, const AttnItem& w, int row0, int lane) {
+        auto keys = [&](int t) { return A.causal ? clampi(t + w.lk - w.lq + 1, 0, w.lk) : w.lk; };
+        const int t0 = sgpr(row0 / A.group), t1 = min(w.lq - 1, sgpr((row0 + 31) / A.group));
+        seen = keys((row0 + (lane & 31)) / A.group);
+        all = keys(t0);
+        any = keys(t1);
+        none = t0 >= w.lq;
+    }
+    // the item's tiles that the wave works on: the first ones
+    template <int BMR, int BN>
+    __device__ __forceinline__ int tiles(const AttnSpan<BMR, BN>& span) const {
+        return none ? 0 : clampi(span.tp + (any + BN - 1) / BN - span.j0, 0, span.n);
+    }
+};
 
 }  // namespace lynx
