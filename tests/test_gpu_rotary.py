@@ -74,6 +74,12 @@ def test_head_sizes_and_axes(D, axes, pairs, ladder):
     run(7, 3, 2, D, axes, pairs=pairs, ladder=ladder, norm=True, weights=True, f32=True)
 
 
+@pytest.mark.parametrize("D", list(range(8, 257, 8)))
+@pytest.mark.parametrize("pairs", ["adjacent", "halves"])
+def test_norm_of_every_head_size(D, pairs):
+    run(5, 9, 2, D, (D // 4 * 2, D // 4 * 2), pairs=pairs, norm=True, weights=True)
+
+
 @pytest.mark.parametrize("T,H,KV", [
     (1, 1, 0), (1, 40, 8), (2, 1, 1), (1000, 1, 0), (333, 5, 1), (17, 24, 24), (4100, 3, 3), (3, 1024, 1024),
 ])
