@@ -12,7 +12,7 @@ namespace {
 
 constexpr int BN = 128, BMR = 32;
 
-template <int DP, bool LSE>
+template <int DP, bool LSE, bool CAUSAL>
 __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs A) {
     constexpr int TILE = 32 * DP * 2;  // a wave's K (or V) of a tile
     constexpr int RING = 128 / DP;
@@ -68,8 +68,12 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs A) {
         W.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         wait_vmcnt<(2 * RING - 1) * PER>();  // V(t)
         asm volatile("" ::: "memory");
-        W.template ahead<false, true>(smem, ka + at, va + at);
-        W.template multiply<false, true>(smem, ka + at, va + at);
+        if (CAUSAL && !pre && view.all < view.any && key0 + 32 > view.all) {
+            W.multiply_hidden(smem, va + at, view.seen - key0);
+        } else {
+            W.template ahead<false, true>(smem, ka + at, va + at);
+            W.template multiply<false, true>(smem, ka + at, va + at);
+        }
         wait_lgkm0();
         asm volatile("" ::: "memory");
         vs.issue(A.D, 0, lane);
@@ -136,13 +140,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs A) {
 
 lynx_status launch_attn_few(const AttnArgs& a, int grid, hipStream_t stream) {
     const dim3 g{unsigned(grid)}, block{256};
-    if (a.lse) {
-        if (a.D <= 64) hipLaunchKernelGGL((attn_few_kernel<64, true>), g, block, 0, stream, a);
-        else hipLaunchKernelGGL((attn_few_kernel<128, true>), g, block, 0, stream, a);
-    } else {
-        if (a.D <= 64) hipLaunchKernelGGL((attn_few_kernel<64, false>), g, block, 0, stream, a);
-        else hipLaunchKernelGGL((attn_few_kernel<128, false>), g, block, 0, stream, a);
-    }
+    auto go = [&](auto dp, auto lse, auto causal) {
+        hipLaunchKernelGGL((attn_few_kernel<dp, lse, causal>), g, block, 0, stream, a);
+    };
+    attn_variant(a, go);
     return launch_status();
 }
 

@@ -13,7 +13,7 @@ namespace {
 
 constexpr int BMR = 128;
 
-template <int DP, bool LSE>
+template <int DP, bool LSE, bool CAUSAL>
 __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs A) {
     constexpr int BN = 8192 / DP, TILE = BN * DP * 2;
     __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];
@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs A) {
         W.init(valid ? A.q + attn_q_offset(A, token, head) : nullptr, A.D);
     }
     const AttnView view(A, w, row0, lane);
-    const int nw = view.tiles(span);
+    const int nw = view.tiles(span), np = CAUSAL ? min(nw, view.plain(span)) : nw;
     const uint32_t ka = W.k_first(), va = W.v_first() + 2 * TILE;
     auto weigh = [&](int t) {
         const int j = span.j0 + t, key0 = span.key(j);
@@ -72,18 +72,29 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs A) {
     };
     uint32_t at = 0;  // of V(t - 1); K(t) has the other slot
     int t = 1;
-    for (; t < nw; ++t) {
+    for (; t < nw && t <= np; ++t) {
         top(t);
         W.template ahead<true, true>(smem, ka + (TILE - at), va + at);
         W.template multiply<true, true>(smem, ka + (TILE - at), va + at);
         weigh(t);
         at = TILE - at;
     }
-    if (nw > 0) {
-        top(t++);
-        W.template ahead<false, true>(smem, ka, va + at);
-        W.template multiply<false, true>(smem, ka, va + at);
+    // tiles that not all rows see whole, and the last one's values
+    for (; t <= nw; ++t) {
+        top(t);
+        if (CAUSAL && t > np) {
+            W.multiply_hidden(smem, va + at, view.seen - span.key(span.j0 + t - 1));
+        } else {
+            W.template ahead<false, true>(smem, ka, va + at);
+            W.template multiply<false, true>(smem, ka, va + at);
+        }
+        if (t == nw) break;
+        W.template ahead<true, false>(smem, ka + (TILE - at), va);
+        W.template multiply<true, false>(smem, ka + (TILE - at), va);
+        weigh(t);
+        at = TILE - at;
     }
+    if (nw > 0) ++t;
     for (; t <= span.n; ++t) top(t);  // tiles that only other waves work on
     wait_vmcnt<0>();                  // loads into LDS end before the workgroup does
     store_rows<DP, LSE>(A, w, W, row0, A.slots > 0 && (A.force_part || w.chunks > 1));
@@ -93,13 +104,10 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs A) {
 
 lynx_status launch_attn_tile(const AttnArgs& a, int grid, hipStream_t stream) {
     const dim3 g{unsigned(grid)}, block{256};
-    if (a.lse) {
-        if (a.D <= 64) hipLaunchKernelGGL((attn_tile_kernel<64, true>), g, block, 0, stream, a);
-        else hipLaunchKernelGGL((attn_tile_kernel<128, true>), g, block, 0, stream, a);
-    } else {
-        if (a.D <= 64) hipLaunchKernelGGL((attn_tile_kernel<64, false>), g, block, 0, stream, a);
-        else hipLaunchKernelGGL((attn_tile_kernel<128, false>), g, block, 0, stream, a);
-    }
+    auto go = [&](auto dp, auto lse, auto causal) {
+        hipLaunchKernelGGL((attn_tile_kernel<dp, lse, causal>), g, block, 0, stream, a);
+    };
+    attn_variant(a, go);
     return launch_status();
 }
 

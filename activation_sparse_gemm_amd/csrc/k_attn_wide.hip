@@ -27,7 +27,7 @@ __device__ __forceinline__ void slot_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int DP, bool LSE>
+template <int DP, bool LSE, bool CAUSAL>
 __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs A) {
     constexpr int BN = 8192 / DP, TILE = BN * DP * 2;
     __shared__ __attribute__((aligned(1024))) char smem[2 * RING * TILE];
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs A) {
         W.init(valid ? A.q + attn_q_offset(A, token, head) : nullptr, A.D);
     }
     const AttnView view(A, w, row0, lane);
-    const int nw = view.tiles(span);
+    const int nw = view.tiles(span), np = CAUSAL ? min(nw, view.plain(span)) : nw;
     const uint32_t ka = W.k_first(), va = W.v_first() + RING * TILE;
     constexpr int PER = ks.PER, EACH = 2 * PER;  // loads of K and V of a tile
     auto load = [&](auto& st, int part) {        // one of two halves
@@ -109,20 +109,34 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs A) {
     }
     m_end();
     if (nw > 0) {
-        for (;;) {
+        while (t + 1 < nw && t < np) {
             weigh(t);
             const uint32_t next = (at + TILE) & (RING * TILE - 1);
-            if (++t == nw) break;
             W.template ahead<true, true>(smem, ka + next, va + at);
             w_end();
             W.template multiply<true, true>(smem, ka + next, va + at);
             m_end();
             at = next;
+            ++t;
         }
-        W.template ahead<false, true>(smem, ka, va + at);
-        w_end();
-        W.template multiply<false, true>(smem, ka, va + at);
-        m_end();
+        // tiles that not all rows see whole, and the last one's values
+        for (; t < nw; ++t) {
+            weigh(t);
+            const uint32_t next = (at + TILE) & (RING * TILE - 1);
+            w_end();
+            if (CAUSAL && t >= np) {
+                W.multiply_hidden(smem, va + at, view.seen - span.key(span.j0 + t));
+            } else {
+                W.template ahead<false, true>(smem, ka, va + at);
+                W.template multiply<false, true>(smem, ka, va + at);
+            }
+            if (t + 1 < nw) {
+                W.template ahead<true, false>(smem, ka + next, va);
+                W.template multiply<true, false>(smem, ka + next, va);
+            }
+            m_end();
+            at = next;
+        }
     }
     for (; t < n; ++t) {  // tiles that only other waves work on
         ks.issue(A.D, wave, lane);
@@ -140,13 +154,10 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs A) {
 
 lynx_status launch_attn_wide(const AttnArgs& a, int grid, hipStream_t stream) {
     const dim3 g{unsigned(grid)}, block{512};
-    if (a.lse) {
-        if (a.D <= 64) hipLaunchKernelGGL((attn_wide_kernel<64, true>), g, block, 0, stream, a);
-        else hipLaunchKernelGGL((attn_wide_kernel<128, true>), g, block, 0, stream, a);
-    } else {
-        if (a.D <= 64) hipLaunchKernelGGL((attn_wide_kernel<64, false>), g, block, 0, stream, a);
-        else hipLaunchKernelGGL((attn_wide_kernel<128, false>), g, block, 0, stream, a);
-    }
+    auto go = [&](auto dp, auto lse, auto causal) {
+        hipLaunchKernelGGL((attn_wide_kernel<dp, lse, causal>), g, block, 0, stream, a);
+    };
+    attn_variant(a, go);
     return launch_status();
 }
 

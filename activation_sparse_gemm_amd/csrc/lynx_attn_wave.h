@@ -301,6 +301,72 @@ struct AttnTile : AttnWave<DP, LSE> {
             __builtin_amdgcn_sched_group_barrier(0x008, products, 0);
         }
     }
+    // The halves of a word of two bf16 that are no finite numbers
+    __device__ __forceinline__ static uint32_t odd_halves(uint32_t w) {
+        return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+    }
+    // O^T += V^T P^T where rows differ in the keys they see (left: how many of the tile's a lane's
+    // row does).  A hidden key's weight is 0, but its value may be infinite or NaN, and 0 times
+    // that is NaN: such values are taken as 0, and added, key by key, to the rows that see them.
+    __device__ __forceinline__ void multiply_hidden(const char* smem, uint32_t v, int left) {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        auto step = [&](int t, u32x4 (&w)[W::DB]) {
+            const char* at = smem + t * (16 * DP * 2);
+#pragma unroll
+            for (int d = 0; d < W::DB; ++d)
+                w[d] = __builtin_bit_cast(u32x4, W::v_pair(at + W::v_at(v, 0, d), at + W::v_at(v, 1, d)));
+        };
+        u32x4 next[W::DB];
+        step(0, next);
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t) {
+            u16x2 top = {0, 0};
+            u32x4 w[W::DB];
+            const u32x4 pw = p[t / 2][t % 2];
+#pragma unroll
+            for (int d = 0; d < W::DB; ++d) w[d] = next[d];
+            if (t + 1 < 2 * NB) step(t + 1, next);
+#pragma unroll
+            for (int d = 0; d < W::DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[d][e] & 0x7F807F80u));
+            if (__ballot(top[0] == 0x7F80 || top[1] == 0x7F80)) {
+#pragma unroll
+                for (int d = 0; d < W::DB; ++d) {
+                    add_odd(w[d], pw, d, left - 16 * t);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[d][e] &= ~odd_halves(w[d][e]);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < W::DB; ++d)
+                W::o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w[d]),
+                                                                 __builtin_bit_cast(bf16x8, pw), W::o[d], 0, 0, 0);
+        }
+    }
+    // The values among w (16 keys, channels 32 d ..) that are no finite numbers, times the weights
+    // pw, to the rows that see them: those with more than the key's number `left`
+    __device__ __forceinline__ void add_odd(const u32x4& w, const u32x4& pw, int d, int left) {
+        for (int k = 0; k < 16; ++k) {  // slot k % 8 of half k / 8
+            u32x4 a, b;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t half = k & 1 ? 0xFFFF0000u : 0xFFFFu;
+                const uint32_t keep = W::h == k >> 3 && e == (k & 7) >> 1 ? half : 0u;
+                a[e] = w[e] & keep & odd_halves(w[e]);
+                b[e] = pw[e] & keep;
+            }
+            f32x16 c;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) c[e] = 0.f;
+            c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+            const bool sees = 4 * (k >> 3) + (k & 3) + 8 * ((k & 7) >> 2) < left;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) W::o[d][e] += sees ? c[e] : 0.f;
+        }
+    }
     // Hides keys from `seen` on; key0: the tile's first
     __device__ __forceinline__ void hide(int key0, int seen) {
 #pragma unroll
@@ -393,11 +459,29 @@ struct AttnView {
         any = keys(t1);
         none = t0 >= w.lq;
     }
+    // of these, the first ones of which the rows see the same keys
+    template <int BMR, int BN>
+    __device__ __forceinline__ int plain(const AttnSpan<BMR, BN>& span) const {
+        return all < any ? clampi(span.tp + all / BN - span.j0, 0, span.n) : span.n;
+    }
     // the item's tiles that the wave works on: the first ones
     template <int BMR, int BN>
     __device__ __forceinline__ int tiles(const AttnSpan<BMR, BN>& span) const {
         return none ? 0 : clampi(span.tp + (any + BN - 1) / BN - span.j0, 0, span.n);
     }
 };
+
+// Calls go(channels, lse, causal) with the constants of the kernel that `a` needs.
+template <class Go>
+void attn_variant(const AttnArgs& a, Go go) {
+    using yes = std::integral_constant<bool, true>;
+    using no = std::integral_constant<bool, false>;
+    auto with = [&](auto dp) {
+        if (a.lse) a.causal ? go(dp, yes{}, yes{}) : go(dp, yes{}, no{});
+        else a.causal ? go(dp, no{}, yes{}) : go(dp, no{}, no{});
+    };
+    if (a.D <= 64) with(std::integral_constant<int, 64>{});
+    else with(std::integral_constant<int, 128>{});
+}
 
 }  // namespace lynx

@@ -269,6 +269,38 @@ def test_query_rows_do_not_meet():
     assert torch.equal(got[~bad], want[~bad])
 
 
+@pytest.mark.parametrize("lq,lk,heads,kv", [(300, 300, 2, 2), (130, 200, 4, 1), (7, 100, 4, 1), (5, 9000, 2, 2),
+                                            (600, 600, 24, 24)])
+@pytest.mark.parametrize("D", [64, 72, 128])
+@pytest.mark.parametrize("P", [0, 40])
+def test_keys_that_are_hidden_may_hold_anything(lq, lk, heads, kv, D, P):
+    """Rows before a key with NaN or infinities get the bytes they get without it; rows that see it
+    what the formula gives: NaN for a key of NaN, and an infinite value in its channel alone."""
+    q, k, v = randn((lq, heads, D), 1), randn((lk, kv, D), 2), randn((lk, kv, D), 3)
+    prefix = (randn((P, kv, D), 4), randn((P, kv, D), 5)) if P else None
+    kw = dict(causal=True, prefix=prefix, return_lse=True)
+    want, wl = lynx.attention(q, k, v, **kw)
+    say(f"hidden keys {lq} {lk} {heads}/{kv}x{D} P={P}")
+    for i in sorted({1, lq // 2, lq - 2, lq - 1}):  # the first query that sees key j
+        j = i + lk - lq
+        a = v.clone()
+        a[j, :, 3], a[j, :, 5], a[j, :, 6] = INF, NAN, -INF
+        out, lse = lynx.attention(q, k, a, **kw)
+        assert torch.equal(lse, wl)
+        assert torch.equal(out[:i], want[:i])
+        others = [c for c in range(D) if c not in (3, 5, 6)]
+        assert torch.equal(out[..., others], want[..., others])
+        assert torch.isnan(out[i:, :, 5]).all()
+        # (inf p: inf, or NaN where p is 0 in bf16)
+        assert not torch.isfinite(out[i:, :, 3]).any() and not (out[i:, :, 3] < 0).any()
+        assert not torch.isfinite(out[i:, :, 6]).any() and not (out[i:, :, 6] > 0).any()
+        b = k.clone()
+        b[j] = NAN
+        out, lse = lynx.attention(q, b, v, **kw)
+        assert torch.equal(out[:i], want[:i]) and torch.equal(lse[:i], wl[:i])
+        assert torch.isnan(out[i:]).all() and torch.isnan(lse[i:]).all()
+
+
 # ---- offsets past 32 bits ----------------------------------------------------------
 
 def test_a_cache_of_more_than_4_gib():
