@@ -14,8 +14,8 @@ constexpr int BN = 128, BMR = 32;
 
 template <int DP, bool LSE, bool CAUSAL>
 __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs A) {
-    constexpr int TILE = 32 * DP * 2;  // a wave's K (or V) of a tile
-    constexpr int RING = 128 / DP;
+    constexpr int TILE = 32 * kRow<DP>;  // a wave's K (or V) of a tile
+    constexpr int RING = 256 / kRow<DP>;
     constexpr int REGS = DP / 2;       // accumulators of a lane
     __shared__ __attribute__((aligned(1024))) char smem[4 * 2 * RING * TILE];
     __shared__ float stat[3][4][32];

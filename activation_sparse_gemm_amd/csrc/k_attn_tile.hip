@@ -15,7 +15,7 @@ constexpr int BMR = 128;
 
 template <int DP, bool LSE, bool CAUSAL>
 __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs A) {
-    constexpr int BN = 8192 / DP, TILE = BN * DP * 2;
+    constexpr int BN = kKeys<DP>, TILE = BN * kRow<DP>;
     __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];
     const uint32_t lds0 = lds_addr(smem);
     const int lane = threadIdx.x & 63;
@@ -55,12 +55,23 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs A) {
     // before every product
     wait_vmcnt<0>();
     block_barrier();
-    ks.issue(A.D, wave, lane);
-    vs.issue(A.D, wave, lane);
+    // The loads of a step are spread over its products: a unit takes 64 bytes a clock, so the four
+    // waves' 32 loads at once hold up each wave for 500 cycles
+    auto loads = [&](int i) {
+        constexpr int PER = ks.PER;
+        if (i == 0) ks.begin(A.D, wave, lane);
+        if (i == 1) vs.begin(A.D, wave, lane);
+#pragma unroll
+        for (int n = 0; n < 2 * PER; ++n)
+            if (i == 1 + n * (W.NM - 1) / (2 * PER)) n < PER ? ks.piece(n) : vs.piece(n - PER);
+    };
     if (nw > 0) {
         W.template ahead<true, false>(smem, ka, va);
-        W.template multiply<true, false>(smem, ka, va);
+        W.template multiply<true, false>(smem, ka, va, loads);
         weigh(0);
+    } else {
+        ks.issue(A.D, wave, lane);
+        vs.issue(A.D, wave, lane);
     }
     auto top = [&](int t) {
         wait_vmcnt<0>();
@@ -73,9 +84,10 @@ __global__ __launch_bounds__(256, 2) void attn_tile_kernel(const AttnArgs A) {
     uint32_t at = 0;  // of V(t - 1); K(t) has the other slot
     int t = 1;
     for (; t < nw && t <= np; ++t) {
-        top(t);
+        wait_vmcnt<0>();
+        block_barrier();
         W.template ahead<true, true>(smem, ka + (TILE - at), va + at);
-        W.template multiply<true, true>(smem, ka + (TILE - at), va + at);
+        W.template multiply<true, true>(smem, ka + (TILE - at), va + at, loads);
         weigh(t);
         at = TILE - at;
     }

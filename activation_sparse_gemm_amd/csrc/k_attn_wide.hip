@@ -29,7 +29,7 @@ __device__ __forceinline__ void slot_barrier() {
 
 template <int DP, bool LSE, bool CAUSAL>
 __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs A) {
-    constexpr int BN = 8192 / DP, TILE = BN * DP * 2;
+    constexpr int BN = kKeys<DP>, TILE = BN * kRow<DP>;
     __shared__ __attribute__((aligned(1024))) char smem[2 * RING * TILE];
     const uint32_t lds0 = lds_addr(smem);
     const int lane = threadIdx.x & 63;

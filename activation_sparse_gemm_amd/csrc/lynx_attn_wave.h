@@ -10,7 +10,8 @@
 // ds_read_b64_tr_b16 transposes it on the way: of 16 lanes, lane i supplies the address of
 // channels 4 (i % 4) .. + 3 of key i / 4, and receives channel i of the four keys.
 //
-// K and V tiles have rows of DP channels (head_dim rounded up; the rest is zero), in 16-byte
+// The kernels are made for DP = 64, 96 and 128 channels (head_dim rounded up; the rest is zero).  K and
+// V tiles have rows of 64 or 128 channels (96 take 25% fewer products than 128), in 16-byte
 // chunks that are permuted within the row so that neither read has bank conflicts.
 #pragma once
 
@@ -20,14 +21,21 @@
 
 namespace lynx {
 
+// bytes of a row in LDS
+template <int DP>
+constexpr int kRow = DP <= 64 ? 128 : 256;
+// keys to a tile: 16 KB of K, and of V
+template <int DP>
+constexpr int kKeys = 16384 / kRow<DP>;
+
 // where chunk c of row r lies in its row
 template <int DP>
 __device__ __forceinline__ int swz_k(int r) {
-    return DP == 128 ? (r & 15) : ((r >> 1) & 7);
+    return kRow<DP> == 256 ? (r & 15) : ((r >> 1) & 7);
 }
 template <int DP>
 __device__ __forceinline__ int swz_v(int r) {
-    return DP == 128 ? ((r & 3) << 2 | ((r >> 2) & 3)) : (((r >> 1) & 1) << 2 | ((r >> 2) & 3));
+    return kRow<DP> == 256 ? ((r & 3) << 2 | ((r >> 2) & 3)) : (((r >> 1) & 1) << 2 | ((r >> 2) & 3));
 }
 
 // The keys that an item works on, in tiles of BN: first those of the prefix (tp tiles), then the
@@ -54,7 +62,7 @@ struct AttnSpan {
 // pieces in turn.  Rows past the item's last tile, and channels from head_dim on, become zero.
 template <int DP, int R, int NW, int RING, bool IS_V>
 struct TileStream {
-    static constexpr int CH = DP / 8, BYTES = R * DP * 2, PER = BYTES / 1024 / NW;
+    static constexpr int CH = kRow<DP> / 16, BYTES = R * kRow<DP>, PER = BYTES / 1024 / NW;
     static_assert(PER * NW * 1024 == BYTES, "");
     uint32_t voff[PER];
     const uint16_t *p, *own;  // the next tile; the sequence's first
@@ -162,15 +170,15 @@ struct AttnWave {
     // permutations are exclusive ors, so the others follow from the first by one instruction.
     __device__ __forceinline__ uint32_t k_first() const {
         const int r = lane & 31;
-        return uint32_t(r) * (DP * 2) + uint32_t((h ^ swz_k<DP>(r)) * 16);
+        return uint32_t(r) * kRow<DP> + uint32_t((h ^ swz_k<DP>(r)) * 16);
     }
     __device__ __forceinline__ static uint32_t k_at(uint32_t first, int i) { return first ^ uint32_t(32 * i); }
     __device__ __forceinline__ uint32_t v_first() const {
         const int i = lane & 15, r = 4 * h + (i >> 2), c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-        return uint32_t(r) * (DP * 2) + uint32_t((c ^ swz_v<DP>(r)) * 16 + 8 * (i & 1));
+        return uint32_t(r) * kRow<DP> + uint32_t((c ^ swz_v<DP>(r)) * 16 + 8 * (i & 1));
     }
     __device__ __forceinline__ static uint32_t v_at(uint32_t first, int u, int db) {
-        return (first ^ uint32_t(64 * db + 32 * u)) + uint32_t(u * 8 * DP * 2);
+        return (first ^ uint32_t(64 * db + 32 * u)) + uint32_t(u * 8 * kRow<DP>);
     }
     __device__ __forceinline__ static bf16x8 v_pair(const char* a, const char* b) {
         const bf16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) bf16x4*)a);
@@ -264,9 +272,9 @@ struct AttnTile : AttnWave<DP, LSE> {
 
     __device__ __forceinline__ void read(const char* smem, uint32_t k, uint32_t v, int i, bool qk, bool pv) {
         if (qk)
-            kf[i] = *reinterpret_cast<const bf16x8*>(smem + W::k_at(k, i / NB) + (i % NB) * (32 * DP * 2));
+            kf[i] = *reinterpret_cast<const bf16x8*>(smem + W::k_at(k, i / NB) + (i % NB) * (32 * kRow<DP>));
         if (pv) {
-            const char* at = smem + (i / W::DB) * (16 * DP * 2);
+            const char* at = smem + (i / W::DB) * (16 * kRow<DP>);
             vf[i] = W::v_pair(at + W::v_at(v, 0, i % W::DB), at + W::v_at(v, 1, i % W::DB));
         }
     }
@@ -275,10 +283,12 @@ struct AttnTile : AttnWave<DP, LSE> {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) read(smem, k, v, i, QK, PV);
     }
-    template <bool QK, bool PV>
-    __device__ __forceinline__ void multiply(const char* smem, uint32_t k, uint32_t v) {
+    // between(i) is called before products i, i = 0 .. NM - 1
+    template <bool QK, bool PV, class Between>
+    __device__ __forceinline__ void multiply(const char* smem, uint32_t k, uint32_t v, Between between) {
 #pragma unroll
         for (int i = 0; i < NM; ++i) {
+            between(i);
             if (i + AHEAD < NM) read(smem, k, v, i + AHEAD, QK, PV);
             if constexpr (QK) {
                 f32x16 c = s[i % NB];
@@ -301,6 +311,11 @@ struct AttnTile : AttnWave<DP, LSE> {
             __builtin_amdgcn_sched_group_barrier(0x008, products, 0);
         }
     }
+    template <bool QK, bool PV>
+    __device__ __forceinline__ void multiply(const char* smem, uint32_t k, uint32_t v) {
+        multiply<QK, PV>(smem, k, v, [](int) {});
+    }
+
     // The halves of a word of two bf16 that are no finite numbers
     __device__ __forceinline__ static uint32_t odd_halves(uint32_t w) {
         return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
@@ -311,7 +326,7 @@ struct AttnTile : AttnWave<DP, LSE> {
     __device__ __forceinline__ void multiply_hidden(const char* smem, uint32_t v, int left) {
         typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
         auto step = [&](int t, u32x4 (&w)[W::DB]) {
-            const char* at = smem + t * (16 * DP * 2);
+            const char* at = smem + t * (16 * kRow<DP>);
 #pragma unroll
             for (int d = 0; d < W::DB; ++d)
                 w[d] = __builtin_bit_cast(u32x4, W::v_pair(at + W::v_at(v, 0, d), at + W::v_at(v, 1, d)));
@@ -417,17 +432,24 @@ __device__ __forceinline__ void store_rows(const AttnArgs& A, const AttnItem& w,
         }
         return;
     }
+    // A lane holds channels 8 g + 4 h .. + 3 of its row: of two groups g, it keeps one and gets its
+    // other half from the row's other lane, 16 bytes to a store
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t* o = A.out + attn_o_offset(A, token, head);
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int at = 32 * d + 8 * g + 4 * W.h;
-            if (at < A.D)
-                *reinterpret_cast<u32x2*>(o + at) =
-                    u32x2{pack_bf16(W.o[d][4 * g] * inv, W.o[d][4 * g + 1] * inv),
-                          pack_bf16(W.o[d][4 * g + 2] * inv, W.o[d][4 * g + 3] * inv)};
+        for (int g = 0; g < 4; g += 2) {
+            uint32_t w[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    w[i][e] = pack_bf16(W.o[d][4 * (g + i) + 2 * e] * inv, W.o[d][4 * (g + i) + 2 * e + 1] * inv);
+            const auto lo = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+            const auto hi = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+            const int at = 32 * d + 8 * (g + W.h);
+            if (at < A.D) *reinterpret_cast<u32x4*>(o + at) = u32x4{lo[0], hi[0], lo[1], hi[1]};
         }
     if (W.h == 0) {
         if constexpr (LSE) A.lse[row] = le == 0.f ? -INFINITY : (W.m + log2f(le)) * kLn2;
@@ -481,6 +503,7 @@ void attn_variant(const AttnArgs& a, Go go) {
         else a.causal ? go(dp, no{}, yes{}) : go(dp, no{}, no{});
     };
     if (a.D <= 64) with(std::integral_constant<int, 64>{});
+    else if (a.D <= 96) with(std::integral_constant<int, 96>{});
     else with(std::integral_constant<int, 128>{});
 }
 
