@@ -1,139 +1,27 @@
-// Attention of few query rows to a key head (lynx_attention): single tokens on caches.  The
-// keys' and values' bytes bound it.  A workgroup holds 32 query rows (tokens x heads in
-// group), its four waves take 32 keys each of a tile of 128 and add up their results at the
-// end.  Each wave stages its own keys and waits for no other wave before the end: K of the next
-// tile is under way while V of this one is multiplied, and the other way round.  Two such
-// workgroups share a compute unit, 64 KB of keys and values under way in each.
-#include "lynx_attn_wave.h"
-#include "lynx_tile.h"
+// Attention of few query rows to a key head, as a kernel of its own; and side by side with tiles
+// of 128 rows, for a prefix that the batch shares: all sequences' rows together on the prefix, each
+// sequence's rows on its own keys.
+#include "lynx_attn_few.h"
+#include "lynx_attn_tile.h"
 
 namespace lynx {
 namespace {
 
-constexpr int BN = 128, BMR = 32;
-
 template <int DP, bool LSE, bool CAUSAL>
 __global__ __launch_bounds__(256, 2) void attn_few_kernel(const AttnArgs A) {
-    constexpr int TILE = 32 * kRow<DP>;  // a wave's K (or V) of a tile
-    constexpr int RING = 256 / kRow<DP>;
-    constexpr int REGS = DP / 2;       // accumulators of a lane
-    __shared__ __attribute__((aligned(1024))) char smem[4 * 2 * RING * TILE];
+    __shared__ __attribute__((aligned(1024))) char smem[65536];
     __shared__ float stat[3][4][32];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    const uint32_t mine = uint32_t(wave) * (2 * RING * TILE);
-    const uint32_t lds0 = lds_addr(smem) + mine;
+    attn_few<DP, LSE, CAUSAL>(A, int(blockIdx.x), smem, stat);
+}
 
-    AttnItem w;
-    if (!attn_item<BMR, BN>(A, w)) return;
-    const AttnSpan<BMR, BN> span(A, w);
-    const int row0 = w.tile * BMR, n = span.n;
-    TileStream<DP, 32, 1, RING, false> ks;
-    TileStream<DP, 32, 1, RING, true> vs;
-    open_stream(ks, A, w, span, false, 32 * wave, lds0, 0, lane);
-    open_stream(vs, A, w, span, true, 32 * wave, lds0 + RING * TILE, 0, lane);
-    // (where the compiler knows of loads of q under way it waits for all loads before every
-    // product, so q is waited for here)
-    ks.issue(A.D, 0, lane);
-    vs.issue(A.D, 0, lane);
-    AttnTile<DP, 32, LSE> W;
-    int token, head;
-    const bool valid = attn_row(A, w, row0 + (lane & 31), token, head);
-    W.init(valid ? A.q + attn_q_offset(A, token, head) : nullptr, A.D);
-    wait_vmcnt<0>();
-#pragma unroll
-    for (int i = 1; i < RING; ++i) {
-        ks.issue(A.D, 0, lane);
-        vs.issue(A.D, 0, lane);
-    }
-    const AttnView view(A, w, row0, lane);
-    const uint32_t ka = mine + W.k_first(), va = mine + RING * TILE + W.v_first();
-    uint32_t at = 0;
-    constexpr int PER = ks.PER;
-    for (int t = 0; t < n; ++t) {
-        // K(t): all but V(t) and the RING - 1 tiles behind it
-        wait_vmcnt<(2 * RING - 1) * PER>();
-        asm volatile("" ::: "memory");
-        W.template ahead<true, false>(smem, ka + at, va + at);
-        W.template multiply<true, false>(smem, ka + at, va + at);
-        wait_lgkm0();
-        asm volatile("" ::: "memory");
-        ks.issue(A.D, 0, lane);
-        const int j = span.j0 + t, key0 = span.key(j) + 32 * wave;
-        const bool pre = j < span.tp;
-        if (key0 + 32 > (pre ? A.prefix : view.all)) W.hide(key0, pre ? A.prefix : view.seen);
-        W.raise(W.maximum(W.s, A.c));
-        float sum[4] = {W.l, 0.f, 0.f, 0.f};
-        W.weights(W.s[0], A.c, W.p[0], sum);
-        W.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        wait_vmcnt<(2 * RING - 1) * PER>();  // V(t)
-        asm volatile("" ::: "memory");
-        if (CAUSAL && !pre && view.all < view.any && key0 + 32 > view.all) {
-            W.multiply_hidden(smem, va + at, view.seen - key0);
-        } else {
-            W.template ahead<false, true>(smem, ka + at, va + at);
-            W.template multiply<false, true>(smem, ka + at, va + at);
-        }
-        wait_lgkm0();
-        asm volatile("" ::: "memory");
-        vs.issue(A.D, 0, lane);
-        at = at == (RING - 1) * TILE ? 0 : at + TILE;
-    }
-    wait_vmcnt<0>();
-
-    // the waves' results: m and l, then o by registers, in the wave's own part
-    const float l = W.both_sum(W.l), le = LSE ? W.both_sum(W.exact) : 0.f;
-    if (W.h == 0) {
-        stat[0][wave][lane] = W.m;
-        stat[1][wave][lane] = l;
-        if constexpr (LSE) stat[2][wave][lane] = le;
-    }
-    float* mo = reinterpret_cast<float*>(smem + mine);
-#pragma unroll
-    for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mo[(16 * d + e) * 64 + lane] = W.o[d][e];
-    __syncthreads();
-    float M = -INFINITY, f[4], lsum = 0.f, esum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) M = fmaxf(M, stat[0][i][lane & 31]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float mi = stat[0][i][lane & 31];
-        f[i] = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mi - M);
-        lsum += f[i] * stat[1][i][lane & 31];
-        if constexpr (LSE) esum += f[i] * stat[2][i][lane & 31];
-    }
-    const bool part = A.slots > 0 && (A.force_part || w.chunks > 1);
-    const int64_t row = int64_t(token) * A.heads + head;
-    const int64_t slot = row * A.slots + A.slot0 + w.chunk;
-    const float inv = part ? 1.f : lsum == 0.f ? 0.f : 1.f / lsum;
-    constexpr int GROUPS = REGS / 4 / 4;  // groups of four channels that a wave finishes
-#pragma unroll
-    for (int gi = 0; gi < GROUPS; ++gi) {
-        const int g = wave * GROUPS + gi, d = 32 * (g / 4) + 8 * (g % 4) + 4 * W.h;
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float* p = reinterpret_cast<const float*>(smem + i * (2 * RING * TILE)) + 4 * g * 64 + lane;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] = fmaf(f[i], p[64 * e], sum[e]);
-        }
-        if (valid && d < A.D) {
-            if (part)
-                *reinterpret_cast<f32x4*>(A.part_o + slot * A.D + d) = sum;
-            else
-                *reinterpret_cast<u32x2*>(A.out + attn_o_offset(A, token, head) + d) =
-                    u32x2{pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv)};
-        }
-    }
-    if (valid && wave == 0 && W.h == 0) {
-        if (part)
-            A.part_ml[slot] = float4{M, lsum, esum, 0.f};
-        else if (LSE)
-            A.lse[row] = esum == 0.f ? -INFINITY : (M + log2f(esum)) * kLn2;
-        if (A.slots > 0 && w.chunk == 0) A.part_n[row] = w.chunks;
-    }
+// The first tile_grid workgroups (a multiple of 8) take the tiles, which take longest.
+template <int DP, bool LSE, bool CAUSAL>
+__global__ __launch_bounds__(256, 2) void attn_pair_kernel(const AttnArgs tile, int tile_grid, const AttnArgs few) {
+    __shared__ __attribute__((aligned(1024))) char smem[65536];
+    __shared__ float stat[3][4][32];
+    const int block = int(blockIdx.x);
+    if (block < tile_grid) attn_tile<DP, LSE, false>(tile, block, smem);
+    else attn_few<DP, LSE, CAUSAL>(few, block - tile_grid, smem, stat);
 }
 
 }  // namespace
@@ -144,6 +32,16 @@ lynx_status launch_attn_few(const AttnArgs& a, int grid, hipStream_t stream) {
         hipLaunchKernelGGL((attn_few_kernel<dp, lse, causal>), g, block, 0, stream, a);
     };
     attn_variant(a, go);
+    return launch_status();
+}
+
+lynx_status launch_attn_pair(const AttnArgs& tile, int tile_grid, const AttnArgs& few, int few_grid,
+                             hipStream_t stream) {
+    const dim3 g{unsigned(tile_grid + few_grid)}, block{256};
+    auto go = [&](auto dp, auto lse, auto causal) {
+        hipLaunchKernelGGL((attn_pair_kernel<dp, lse, causal>), g, block, 0, stream, tile, tile_grid, few);
+    };
+    attn_variant(few, go);
     return launch_status();
 }
 

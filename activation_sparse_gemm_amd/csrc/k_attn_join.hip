@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs A, int pr
     if (n == 0) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (in) {
-        const int b = token / A.addr_len;
+        const int b = A.addr_len == 0 ? 0 : token / A.addr_len;
         uint16_t* out = A.out + b * A.o_b + (token - b * A.addr_len) * A.o_t + head * A.o_h + c;
         *reinterpret_cast<u32x2*>(out) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
     }

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs A) {
     const int group = wave >> 2;
 
     AttnItem w;
-    if (!attn_item<BMR, BN>(A, w)) return;
+    if (!attn_item<BMR, BN>(A, int(blockIdx.x), w)) return;
     const AttnSpan<BMR, BN> span(A, w);
     const int row0 = w.tile * BMR + wave * 32, n = span.n;
     TileStream<DP, BN, 8, RING, false> ks;

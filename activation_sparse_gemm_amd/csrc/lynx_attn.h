@@ -33,15 +33,17 @@ struct AttnArgs {
     float* lse;
     float* part_o;    // [row][slot][D]
     float4* part_ml;  // [row][slot]: m in powers of two, l, l of unrounded weights (with lse)
-    int* part_n;      // [row]
+    int* part_n;      // [row]; NULL in the pass over a prefix, whose chunks are the same for all rows
     int64_t q_b, q_t, q_h, o_b, o_t, o_h;
     int64_t k_b, k_t, k_h, v_b, v_t, v_h, pk_t, pk_h, pv_t, pv_h;
     int batch, heads, kv_heads, group, D;
     int tokens_q, tokens_k, prefix;
     int len_q, len_k;    // uniform form: tokens of a sequence
-    int addr_len;        // tokens of q and out that are q_t apart
+    int addr_len;        // tokens of q and out that are q_t apart; 0: all
     int slots, slot0, force_part, chunk_tiles, chunk_max;
     int classes;         // gcd(kv_heads, 8)
+    int group_shift;     // log2(group), or -1
+    int pieces;          // uniform form: pieces of a sequence to a key head
     float c;             // scale * log2(e)
     int causal;
 };
@@ -61,10 +63,15 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v,
 // a value that every lane holds, as a scalar
 __device__ __forceinline__ int sgpr(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// inclusive sum over the lanes of a wave
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
+// token of a row number (a division costs 30 instructions)
+__device__ __forceinline__ int row_token(const AttnArgs& A, int row) {
+    return A.group_shift >= 0 ? row >> A.group_shift : row / A.group;
+}
+
+// inclusive sum over the first n lanes of a wave (those behind them hold 0: the last lane has
+// the whole sum)
+__device__ __forceinline__ int wave_scan(int v, int lane, int n) {
+    for (int d = 1; d < min(n, 64); d *= 2) {
         const int o = __shfl_up(v, d);
         if (lane >= d) v += o;
     }
@@ -75,27 +82,29 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
 template <int BM, int BN>
 struct AttnPlan {
     int tiles, chunks, per;  // per: key tiles of a chunk
-    __device__ __forceinline__ AttnPlan(const AttnArgs& A, int lq, int lk) {
+    template <class Args>
+    __host__ __device__ __forceinline__ AttnPlan(const Args& A, int lq, int lk) {
         tiles = (lq * A.group + BM - 1) / BM;
         const int kt = (A.prefix + BN - 1) / BN + (lk + BN - 1) / BN;
         if (A.chunk_max == 1) {
-            per = max(kt, 1);
+            per = kt > 1 ? kt : 1;
             chunks = 1;
         } else {
-            per = max(A.chunk_tiles, (kt + A.chunk_max - 1) / A.chunk_max);
-            chunks = max(1, (kt + per - 1) / per);
+            per = (kt + A.chunk_max - 1) / A.chunk_max;
+            if (per < A.chunk_tiles) per = A.chunk_tiles;
+            chunks = kt > 0 ? (kt + per - 1) / per : 1;
         }
     }
 };
 
-// The piece of work of this workgroup; false if there is none.  Uniform over the workgroup.
+// The piece of work of workgroup `block`; false if there is none.  Uniform over the workgroup.
 // Workgroups of one XCD (their number mod 8) take the same key heads, one after the other, so that
 // its L2 holds the keys and values that its workgroups read; where there are fewer key heads than
 // XCDs several share a head.  Within a head sequences follow one another, and a sequence's row tiles
 // come last tile first: under a causal mask these have the most keys, and the light ones fill the
 // end.
 template <int BM, int BN>
-__device__ __forceinline__ bool attn_item(const AttnArgs& A, AttnItem& w) {
+__device__ __forceinline__ bool attn_item(const AttnArgs& A, int block, AttnItem& w) {
     const int lane = threadIdx.x & 63;
     // of sequence s: its range of tokens, and how many pieces it has to a key head
     struct Range {
@@ -113,32 +122,33 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& A, AttnItem& w) {
         const AttnPlan<BM, BN> p(A, r.lq, r.lk);
         return p.tiles * p.chunks;
     };
-    Range mine = {0, A.len_q, 0, A.len_k};
+    const int xcd = block & 7, slot = block >> 3, share = 8 / A.classes;
+    const int idx = slot * share + xcd / A.classes;
+    Range mine = {0, 0, 0, 0};
     int per_head, sum = 0;  // pieces to a key head; of the sequences up to this lane's (the first 64)
     if (A.cu_q) {
         if (lane < A.batch) {
             mine = range(lane);
             sum = pieces(mine);
         }
-        sum = wave_scan(sum, lane);
-        per_head = __builtin_amdgcn_readlane(sum, 63);
+        sum = wave_scan(sum, lane, A.batch);
+        per_head = __builtin_amdgcn_readlane(sum, min(A.batch, 64) - 1);
         if (A.batch > 64) {
             int n = 0;
             for (int s = 64 + lane; s < A.batch; s += 64) n += pieces(range(s));
-            per_head += __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
+            per_head += __builtin_amdgcn_readlane(wave_scan(n, lane, 64), 63);
         }
     } else {
-        per_head = sgpr(A.batch * pieces(mine));
+        per_head = A.batch * A.pieces;
     }
     if (per_head == 0) return false;
-    const int xcd = int(blockIdx.x) & 7, slot = int(blockIdx.x) >> 3, share = 8 / A.classes;
-    const int idx = slot * share + xcd / A.classes, hi = sgpr(idx / per_head);
+    const int hi = A.kv_heads == A.classes ? (idx < per_head ? 0 : 1) : sgpr(idx / per_head);
     if (hi >= A.kv_heads / A.classes) return false;
-    w.kvh = sgpr(xcd % A.classes + A.classes * hi);
+    w.kvh = xcd % A.classes + A.classes * hi;
     int r = idx - hi * per_head;
     if (A.cu_q) {
         int before = 0, base = 0;  // pieces before lane 0's sequence, and that sequence
-        uint64_t over = __ballot(sum > r);
+        uint64_t over = __ballot(lane < A.batch && sum > r);
         while (over == 0) {
             before += __builtin_amdgcn_readlane(sum, 63);
             base += 64;
@@ -148,7 +158,7 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& A, AttnItem& w) {
                 mine = range(base + lane);
                 sum = pieces(mine);
             }
-            sum = wave_scan(sum, lane);
+            sum = wave_scan(sum, lane, 64);
             over = __ballot(before + sum > r);
         }
         const int l = __builtin_ctzll(over);
@@ -160,9 +170,8 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& A, AttnItem& w) {
         w.k0 = __builtin_amdgcn_readlane(mine.k0, l);
         w.lk = __builtin_amdgcn_readlane(mine.lk, l);
     } else {
-        const int per = sgpr(pieces(mine));
-        w.seq = sgpr(r / per);
-        r -= w.seq * per;
+        w.seq = A.batch == 1 ? 0 : sgpr(r / A.pieces);
+        r -= w.seq * A.pieces;
         w.q0 = w.seq * A.len_q;
         w.lq = A.len_q;
         w.k0 = 0;
@@ -171,7 +180,7 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& A, AttnItem& w) {
     const AttnPlan<BM, BN> p(A, w.lq, w.lk);
     const int tiles = sgpr(p.tiles);
     w.chunks = sgpr(p.chunks);
-    w.chunk = sgpr(r / tiles);
+    w.chunk = w.chunks == 1 ? 0 : sgpr(r / tiles);
     w.tile = tiles - 1 - (r - w.chunk * tiles);
     return true;
 }
@@ -182,6 +191,9 @@ lynx_status launch_qk_rotary(const lynx_rotary& d, hipStream_t stream);
 lynx_status launch_attn_tile(const AttnArgs& a, int grid, hipStream_t stream);
 lynx_status launch_attn_wide(const AttnArgs& a, int grid, hipStream_t stream);
 lynx_status launch_attn_few(const AttnArgs& a, int grid, hipStream_t stream);
+// `tile` (not causal) and `few` side by side, in one launch
+lynx_status launch_attn_pair(const AttnArgs& tile, int tile_grid, const AttnArgs& few, int few_grid,
+                             hipStream_t stream);
 lynx_status launch_attn_join(const AttnArgs& a, int prefix_slots, hipStream_t stream);
 
 }  // namespace lynx

@@ -303,12 +303,26 @@ lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t worksp
     a.tokens_k = int(d.tokens_k);
     a.len_q = int(d.tokens_q / d.batch);
     a.len_k = int(d.tokens_k / d.batch);
-    a.addr_len = d.cu_q ? INT32_MAX : a.len_q;
+    a.addr_len = d.cu_q || d.batch == 1 ? 0 : a.len_q;
+    a.group_shift = (a.group & (a.group - 1)) == 0 ? __builtin_ctz(unsigned(a.group)) : -1;
     a.slots = P.slots;
     a.classes = int(std::gcd<int64_t>(d.kv_heads, 8));
     a.c = d.scale * kLog2e;
     a.causal = d.causal != 0;
 
+    // a pass' arguments, and its launch
+    auto cut = [&](AttnArgs& args, const Pass& p) {
+        args.chunk_tiles = p.chunk_tiles;
+        args.chunk_max = p.chunk_max;
+        auto pieces = [&](auto plan) { return plan.tiles * plan.chunks; };
+        const bool small = args.D <= 64;  // (tiles of keys are 128 then)
+        args.pieces = p.kernel == Kernel::few ? pieces(AttnPlan<32, 128>(args, args.len_q, args.len_k))
+                      : p.kernel == Kernel::tile
+                          ? (small ? pieces(AttnPlan<128, 128>(args, args.len_q, args.len_k))
+                                   : pieces(AttnPlan<128, 64>(args, args.len_q, args.len_k)))
+                          : (small ? pieces(AttnPlan<256, 128>(args, args.len_q, args.len_k))
+                                   : pieces(AttnPlan<256, 64>(args, args.len_q, args.len_k)));
+    };
     auto run = [&](const AttnArgs& args, const Pass& p) {
         switch (p.kernel) {
             case Kernel::few: return launch_attn_few(args, int(p.grid), s);
@@ -316,8 +330,8 @@ lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t worksp
             default: return launch_attn_wide(args, int(p.grid), s);
         }
     };
+    AttnArgs p = a;
     if (P.apart) {
-        AttnArgs p = a;
         p.k = d.prefix_k;
         p.v = d.prefix_v;
         p.cu_q = p.cu_k = nullptr;
@@ -331,10 +345,8 @@ lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t worksp
         p.tokens_k = p.len_k = int(d.prefix_tokens);
         p.causal = 0;
         p.force_part = 1;
-        p.chunk_tiles = P.prefix.chunk_tiles;
-        p.chunk_max = P.prefix.chunk_max;
-        st = run(p, P.prefix);
-        if (st != LYNX_OK) return st;
+        p.part_n = nullptr;
+        cut(p, P.prefix);
         a.slot0 = P.prefix.chunk_max;
         a.force_part = 1;
     } else {
@@ -346,9 +358,13 @@ lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t worksp
         a.pv_h = d.prefix_v_head_stride;
         a.prefix = int(d.prefix_tokens);
     }
-    a.chunk_tiles = P.own.chunk_tiles;
-    a.chunk_max = P.own.chunk_max;
-    st = run(a, P.own);
+    cut(a, P.own);
+    if (P.apart && P.prefix.kernel == Kernel::tile && P.own.kernel == Kernel::few) {
+        st = launch_attn_pair(p, int(P.prefix.grid), a, int(P.own.grid), s);
+    } else {
+        if (P.apart) st = run(p, P.prefix);
+        if (st == LYNX_OK) st = run(a, P.own);
+    }
     if (st != LYNX_OK) return st;
     if (P.slots > 0) {
         st = launch_attn_join(a, a.slot0, s);

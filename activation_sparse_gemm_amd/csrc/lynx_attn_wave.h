@@ -47,7 +47,7 @@ struct AttnSpan {
         const AttnPlan<BMR, BN> plan(A, w.lq, w.lk);
         const int per = sgpr(plan.per);
         // up to the last own key that the last query of the row tile sees
-        const int last = min(w.lq - 1, sgpr((w.tile * BMR + BMR - 1) / A.group));
+        const int last = min(w.lq - 1, sgpr(row_token(A, w.tile * BMR + BMR - 1)));
         const int own = A.causal ? clampi(last + w.lk - w.lq + 1, 0, w.lk) : w.lk;
         tp = (A.prefix + BN - 1) / BN;
         j0 = w.chunk * per;
@@ -392,16 +392,18 @@ struct AttnTile : AttnWave<DP, LSE> {
 // The query row's place: token and head of row `row` of an item, or false where there is none.
 __device__ __forceinline__ bool attn_row(const AttnArgs& A, const AttnItem& w, int row, int& token,
                                          int& head) {
-    const int t = row / A.group;
+    const int t = row_token(A, row);
     token = w.q0 + t;
     head = w.kvh * A.group + (row - t * A.group);
     return t < w.lq;
 }
 __device__ __forceinline__ int64_t attn_q_offset(const AttnArgs& A, int token, int head) {
+    if (A.addr_len == 0) return token * A.q_t + head * A.q_h;
     const int b = token / A.addr_len;
     return b * A.q_b + (token - b * A.addr_len) * A.q_t + head * A.q_h;
 }
 __device__ __forceinline__ int64_t attn_o_offset(const AttnArgs& A, int token, int head) {
+    if (A.addr_len == 0) return token * A.o_t + head * A.o_h;
     const int b = token / A.addr_len;
     return b * A.o_b + (token - b * A.addr_len) * A.o_t + head * A.o_h;
 }
@@ -428,7 +430,7 @@ __device__ __forceinline__ void store_rows(const AttnArgs& A, const AttnItem& w,
             }
         if (W.h == 0) {
             A.part_ml[slot] = float4{W.m, l, le, 0.f};
-            if (w.chunk == 0) A.part_n[row] = w.chunks;
+            if (w.chunk == 0 && A.part_n) A.part_n[row] = w.chunks;
         }
         return;
     }
@@ -475,8 +477,8 @@ struct AttnView {
     bool none;
     __device__ __forceinline__ AttnView(const AttnArgs& A, const AttnItem& w, int row0, int lane) {
         auto keys = [&](int t) { return A.causal ? clampi(t + w.lk - w.lq + 1, 0, w.lk) : w.lk; };
-        const int t0 = sgpr(row0 / A.group), t1 = min(w.lq - 1, sgpr((row0 + 31) / A.group));
-        seen = keys((row0 + (lane & 31)) / A.group);
+        const int t0 = sgpr(row_token(A, row0)), t1 = min(w.lq - 1, sgpr(row_token(A, row0 + 31)));
+        seen = keys(row_token(A, row0 + (lane & 31)));
         all = keys(t0);
         any = keys(t1);
         none = t0 >= w.lq;
