@@ -17,6 +17,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 constexpr int kMaxChunks = 128;  // of a pass
+constexpr int kNearTiles = 5;    // of keys, that the kernel for few keys has room for
 
 // Arguments of an attention kernel.  Query rows of one sequence and key head are numbered
 // token * group + head in group, so that the heads that share a key head share its tiles.
@@ -43,7 +44,7 @@ struct AttnArgs {
     int slots, slot0, force_part, chunk_tiles, chunk_max;
     int classes;         // gcd(kv_heads, 8)
     int group_shift;     // log2(group), or -1
-    int pieces;          // uniform form: pieces of a sequence to a key head
+    int pieces;          // uniform form: pieces of a sequence to a key head (few keys: shares of its rows)
     float c;             // scale * log2(e)
     int causal;
 };
@@ -191,6 +192,7 @@ lynx_status launch_qk_rotary(const lynx_rotary& d, hipStream_t stream);
 lynx_status launch_attn_tile(const AttnArgs& a, int grid, hipStream_t stream);
 lynx_status launch_attn_wide(const AttnArgs& a, int grid, hipStream_t stream);
 lynx_status launch_attn_few(const AttnArgs& a, int grid, hipStream_t stream);
+lynx_status launch_attn_near(const AttnArgs& a, int grid, hipStream_t stream);
 // `tile` (not causal) and `few` side by side, in one launch
 lynx_status launch_attn_pair(const AttnArgs& tile, int tile_grid, const AttnArgs& few, int few_grid,
                              hipStream_t stream);

@@ -104,11 +104,12 @@ lynx_status validate_attn(const lynx_attn& d, bool* noop) {
 }
 
 // One launch over keys: which kernel, and how keys are cut.
-enum class Kernel { few, tile, wide };
+enum class Kernel { few, near, tile, wide };
 struct Pass {
     Kernel kernel;
     int chunk_tiles, chunk_max;  // as in AttnArgs; chunk_max 1: not cut
     int64_t grid;
+    int shares;  // near: of a sequence's rows
 };
 
 struct Plan {
@@ -174,6 +175,7 @@ Pass plan_pass(int64_t batch, int64_t rows, int64_t keys, int64_t shared, int64_
     const int64_t bn = D <= 64 ? 128 : 64;
     const int64_t kt = ((keys + batch - 1) / batch + shared + bn - 1) / bn;
     double best = 0.0;
+    double besides = 0.0;  // what the best's row tiles take besides, as the kernel for few keys sees it
     // (packed sequences differ: the 256-row tiles of a long one end late)
     for (int wide = 0; wide < (ragged && batch > 1 ? 1 : 2); ++wide) {
         const int64_t bm = wide ? 256 : 128, tiles = tiles_of(bm);
@@ -189,9 +191,31 @@ Pass plan_pass(int64_t batch, int64_t rows, int64_t keys, int64_t shared, int64_
             else if (chunks > 1) us += 4.0 + double(row_bytes * chunks) * 2.0 / 4.0e6;
             if (best == 0.0 || us < best) {
                 best = us;
+                besides = double((items + kUnits - 1) / kUnits) * (wide ? 7.0 : 3.5);
                 finish(wide ? Kernel::wide : Kernel::tile, bm, bn, per, chunks == 1 ? 0 : chunks);
             }
             if (items >= 8 * kUnits) break;
+        }
+    }
+    // Few keys, the same for all sequences: the kernel that holds them all in LDS.  To it, 256 rows
+    // and a tile of keys are 2.3 us, and there are 5 us besides for a workgroup; to the others, 3.5 us
+    // (wide: 7) besides for each row tile that a unit takes.  4608 x 256 x 24 heads 26 us (34), 20000 x 300
+    // x 28 heads 120 (179); on the other side 1024 x 300 x 24 heads 17 us (12, and that is taken).
+    if (!ragged && seen == 1.0 && shared == 0 && !joined && kt >= 1 && kt <= kNearTiles) {
+        const int64_t pairs = batch * kv_heads, tiles = (mean_rows + 31) / 32;
+        best += besides;
+        for (int64_t shares = 1; shares <= (tiles + 7) / 8; ++shares) {
+            if (shares > 1 && pairs * shares > 8 * kUnits) break;
+            const int64_t per = (tiles + shares - 1) / shares;
+            const double us = double((pairs * shares + kUnits - 1) / kUnits) *
+                              (5.0 + double((per + 7) / 8) * double(kt) * 2.3);
+            if (us >= best) continue;
+            best = us;
+            p.kernel = Kernel::near;
+            p.chunk_tiles = int(kt);
+            p.chunk_max = 1;
+            p.shares = int(shares);
+            p.grid = pairs * shares;
         }
     }
     return p;
@@ -316,7 +340,8 @@ lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t worksp
         args.chunk_max = p.chunk_max;
         auto pieces = [&](auto plan) { return plan.tiles * plan.chunks; };
         const bool small = args.D <= 64;  // (tiles of keys are 128 then)
-        args.pieces = p.kernel == Kernel::few ? pieces(AttnPlan<32, 128>(args, args.len_q, args.len_k))
+        args.pieces = p.kernel == Kernel::near  ? p.shares
+                      : p.kernel == Kernel::few ? pieces(AttnPlan<32, 128>(args, args.len_q, args.len_k))
                       : p.kernel == Kernel::tile
                           ? (small ? pieces(AttnPlan<128, 128>(args, args.len_q, args.len_k))
                                    : pieces(AttnPlan<128, 64>(args, args.len_q, args.len_k)))
@@ -326,6 +351,7 @@ lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t worksp
     auto run = [&](const AttnArgs& args, const Pass& p) {
         switch (p.kernel) {
             case Kernel::few: return launch_attn_few(args, int(p.grid), s);
+            case Kernel::near: return launch_attn_near(args, int(p.grid), s);
             case Kernel::tile: return launch_attn_tile(args, int(p.grid), s);
             default: return launch_attn_wide(args, int(p.grid), s);
         }

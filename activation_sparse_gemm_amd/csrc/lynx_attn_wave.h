@@ -150,18 +150,24 @@ struct AttnWave {
     __device__ __forceinline__ void init(const uint16_t* p, int D) {
         lane = threadIdx.x & 63;
         h = lane >> 5;
+        clear();
+        read_q(q, p, D);
+    }
+    __device__ __forceinline__ void clear() {
         m = -INFINITY;
         l = exact = 0.f;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+    }
+    __device__ __forceinline__ void read_q(bf16x8 (&to)[KS], const uint16_t* p, int D) const {
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int d = 16 * s + 8 * h;
             u32x4 v = {};
             if (p && d < D) v = *reinterpret_cast<const u32x4*>(p + d);
-            q[s] = __builtin_bit_cast(bf16x8, v);
+            to[s] = __builtin_bit_cast(bf16x8, v);
         }
     }
 

@@ -183,6 +183,40 @@ def test_uniform_batches_and_strides(B, Lq, Lk, heads, kv, D, causal, layout):
     check(out, lse, ref, D, Lk)
 
 
+@pytest.mark.parametrize("B,Lq,Lk,heads,kv,D", [
+    (2, 4100, 300, 16, 16, 72), (5, 2011, 1, 16, 4, 128), (3, 3001, 640, 12, 12, 64), (1, 4609, 77, 24, 3, 40),
+    (1, 9000, 320, 14, 2, 128), (70, 131, 33, 16, 8, 96), (1, 8200, 65, 32, 8, 128), (300, 260, 64, 2, 2, 8),
+])
+@pytest.mark.parametrize("layout", ["BSHD", "BHSD"])
+def test_many_rows_on_few_keys(B, Lq, Lk, heads, kv, D, layout):
+    def make(L, h, seed, size=1.6):
+        if layout == "BHSD":
+            return randn((B, h, L, D), seed, size).transpose(1, 2)
+        return randn((B, L, h + 1, D + 8), seed, size)[:, :, 1:, 8:]
+
+    q, k, v = make(Lq, heads, 1), make(Lk, kv, 2), make(Lk, kv, 3, 1.0)
+    some = sorted({0, 1, 31, 32, 33, Lq // 2, Lq - 33, Lq - 32, Lq - 2, Lq - 1})
+    ref = ao.attention(host_f64(q[:, some]).reshape(-1, heads, D),
+                       *(host_f64(t).reshape(-1, kv, D) for t in (k, v)), [len(some)] * B, [Lk] * B, False)
+    say(f"few keys {layout} {B}x{Lq}x{Lk} {heads}/{kv}x{D}")
+    kw = poisoned(q, B, B * Lk, kv, 0, False)
+    if layout == "BHSD":
+        kw["out"] = nan_bf16((B, heads, Lq, D)).transpose(1, 2)
+    out, lse = lynx.attention(q, k, v, **kw)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    check(out[:, some], lse[:, some], ref, D, Lk)
+    # other rows, as a call of few rows, which another kernel takes: twice the bounds above, with
+    # dev <= 2 max |v| and magnitudes of a score <= scale |q| |k|
+    n = min(500, Lq)
+    other, lother = lynx.attention(q[:1, :n], k[:1], v[:1], return_lse=True)
+    spread = (q[:1, :n].float().norm(dim=-1).max() * k[:1].float().norm(dim=-1).max()).item() * D ** -0.5
+    err_s = (D * 2.0 ** -23 + 2.0 ** -22) * spread + 2.0 ** -21
+    top = 3 * v[:1].float().abs().max().item()
+    assert (out[0, :n].float() - other[0].float()).abs().max() <= 2 * (2.0 ** -8 + 2 * err_s + Lk * 2.0 ** -23) * top
+    assert (lse[0, :n] - lother[0]).abs().max() <= \
+        2 * (err_s + Lk * 2.0 ** -23 + 2.0 ** -22 * lother[0].abs().max().item())
+
+
 def test_heads_may_share_memory():
     q, k = randn((100, 6, 64), 1), randn((100, 1, 64), 2)
     v = randn((100, 1, 64), 3)
