@@ -92,7 +92,10 @@ struct AttnPlan {
             chunks = 1;
         } else {
             per = (kt + A.chunk_max - 1) / A.chunk_max;
-            if (per < A.chunk_tiles) per = A.chunk_tiles;
+            // (few rows: longer chunks where a sequence has several row tiles after all, so that
+            // these do not add to the length of the work list)
+            const int64_t least = int64_t(A.chunk_tiles) * (BM == 32 ? tiles : 1);
+            if (per < least) per = least < kt ? int(least) : kt;
             chunks = kt > 0 ? (kt + per - 1) / per : 1;
         }
     }

@@ -146,7 +146,7 @@ Pass plan_pass(int64_t batch, int64_t rows, int64_t keys, int64_t shared, int64_
         if (ragged) {
             const int64_t all = keys / bn + batch * (1 + (shared + bn - 1) / bn);
             items = (rows / bm + batch) * top;
-            items = std::min(items, all / per + batch + rows / bm * top);
+            items = std::min(items, all / per + batch + rows / bm * (kernel == Kernel::few ? 1 : top));
         }
         const int64_t classes = std::gcd<int64_t>(kv_heads, 8), share = 8 / classes;
         p.grid = 8 * ((kv_heads / classes * items + share - 1) / share);
