@@ -123,9 +123,10 @@ constexpr int kUnits = 256;
 
 // Which kernel takes a pass, and into how many chunks it cuts the keys.  rows: query rows to a
 // key head, over all sequences; keys: of all sequences together; shared: keys that each sequence has
-// besides; seen: the share of the keys that a mask leaves; joined: whether the join runs anyway.
+// besides; seen: the share of the keys that a mask leaves; joined: whether the join runs anyway;
+// beside: workgroups of the few-row kernel that run side by side with this pass.
 Pass plan_pass(int64_t batch, int64_t rows, int64_t keys, int64_t shared, int64_t kv_heads, int64_t D,
-               bool ragged, double seen, bool joined) {
+               bool ragged, double seen, bool joined, int64_t beside) {
     Pass p = {};
     constexpr int64_t kMaxPartial = int64_t(1) << 28;
     const int64_t mean_rows = (rows + batch - 1) / batch, row_bytes = kv_heads * rows * (D * 4 + 16);
@@ -189,6 +190,13 @@ Pass plan_pass(int64_t batch, int64_t rows, int64_t keys, int64_t shared, int64_
                               double(per) * step * (wide || items <= kUnits ? 1.0 : 1.6));
             if (joined) us += double(row_bytes * chunks) * 2.0 / 4.0e6;
             else if (chunks > 1) us += 4.0 + double(row_bytes * chunks) * 2.0 / 4.0e6;
+            // The few-row kernel runs beside the tile kernel, but after the wide one.  Units have room
+            // for two workgroups: where that is enough for the few-row kernel's alone, those
+            // that have to wait for a tile end late (48 tokens on a prefix of 8192: 10 chunks
+            // 31 us, 16 39; 48 x 4 on 4096: wide 52, tile 35).
+            const int64_t over = items + beside - 2 * kUnits;
+            if (beside > 0 && wide) us += 14.0;
+            else if (beside > 0 && beside <= 2 * kUnits && over > 0) us += 14.0 * std::min(1.0, double(over) / 256.0);
             if (best == 0.0 || us < best) {
                 best = us;
                 besides = double((items + kUnits - 1) / kUnits) * (wide ? 7.0 : 3.5);
@@ -235,10 +243,11 @@ Plan make_plan(const lynx_attn& d, bool ragged) {
         const double keys = double(d.tokens_k) + double(d.batch) * double(shared);
         if (keys > 0.0) seen = std::max(0.5, 1.0 - 0.5 * double(d.tokens_q) / keys);
     }
-    P.own = plan_pass(d.batch, rows, d.tokens_k, shared, d.kv_heads, d.head_dim, ragged, seen, P.apart);
+    P.own = plan_pass(d.batch, rows, d.tokens_k, shared, d.kv_heads, d.head_dim, ragged, seen, P.apart, 0);
     int slots = P.own.chunk_max > 1 ? P.own.chunk_max : 0;
     if (P.apart) {
-        P.prefix = plan_pass(1, rows, d.prefix_tokens, 0, d.kv_heads, d.head_dim, false, 1.0, true);
+        const int64_t pairs = P.own.kernel == Kernel::few ? d.batch * d.kv_heads : 0;
+        P.prefix = plan_pass(1, rows, d.prefix_tokens, 0, d.kv_heads, d.head_dim, false, 1.0, true, pairs);
         slots = P.own.chunk_max + P.prefix.chunk_max;
     }
     P.slots = slots;
