@@ -673,12 +673,12 @@ def qk_rotary(q, k, positions, axes, theta=10000.0, pairs="adjacent", ladder="ax
 
 
 def attention_workspace_bytes(batch, tokens_q, tokens_k, heads, kv_heads, head_dim,
-                              prefix_tokens=0, packed=False) -> int:
+                              prefix_tokens=0, packed=False, causal=False) -> int:
     """lynx_attention_workspace_bytes; tokens over all sequences, packed: with offsets."""
     cu = 4 if packed else 0
     return lib().lynx_attention_workspace_bytes(
         _ATTN.pack(0, 0, 0, 0, 0, cu, cu, 0, 0, batch, tokens_q, tokens_k, prefix_tokens, heads,
-                   kv_heads, head_dim, *(0,) * 16, 1.0, 0))
+                   kv_heads, head_dim, *(0,) * 16, 1.0, bool(causal)))
 
 
 def attention(q, k, v, cu_q=None, cu_k=None, causal=False, scale=None, prefix=None,

@@ -13,8 +13,9 @@ namespace {
 
 constexpr int64_t kMaxRotaryTokens = int64_t(1) << 24, kMaxHeads = 1024;
 constexpr int64_t kMaxAttnTokens = int64_t(1) << 26, kMaxBatch = int64_t(1) << 16;
-constexpr int64_t kMaxTokenStride = int64_t(1) << 24;  // 64 rows stay below 2^31 bytes
+constexpr int64_t kMaxTokenStride = int64_t(1) << 23;  // a tile's 128 rows stay below 2^31 bytes
 constexpr int64_t kMaxQueryRows = int64_t(1) << 30;
+constexpr int64_t kMaxPairs = int64_t(1) << 21;  // sequences times key heads: a launch has below 2^32 threads
 
 bool all16(std::initializer_list<const void*> ps) {
     for (const void* p : ps)
@@ -66,7 +67,7 @@ lynx_status validate_rotary(const lynx_rotary& d, bool* noop) {
 bool attn_sizes_ok(const lynx_attn& d) {
     if (d.head_dim < 8 || d.head_dim > 128 || d.head_dim % 8 != 0) return false;
     if (d.kv_heads < 1 || d.heads < 1 || d.heads > kMaxHeads || d.heads % d.kv_heads != 0) return false;
-    if (d.batch < 1 || d.batch > kMaxBatch) return false;
+    if (d.batch < 1 || d.batch > kMaxBatch || d.batch * d.kv_heads > kMaxPairs) return false;
     for (int64_t t : {d.tokens_q, d.tokens_k, d.prefix_tokens})
         if (t < 0 || t > kMaxAttnTokens) return false;
     return d.tokens_q * d.heads < kMaxQueryRows;
@@ -212,11 +213,12 @@ Pass plan_pass(int64_t batch, int64_t rows, int64_t keys, int64_t shared, int64_
     if (!ragged && seen == 1.0 && shared == 0 && !joined && kt >= 1 && kt <= kNearTiles) {
         const int64_t pairs = batch * kv_heads, tiles = (mean_rows + 31) / 32;
         best += besides;
-        for (int64_t shares = 1; shares <= (tiles + 7) / 8; ++shares) {
-            if (shares > 1 && pairs * shares > 8 * kUnits) break;
-            const int64_t per = (tiles + shares - 1) / shares;
+        for (int64_t r = 1; r <= 4; ++r) {  // workgroups to a unit
+            int64_t shares = std::max<int64_t>(1, std::min(r * kUnits / pairs, (tiles + 7) / 8));
+            const int64_t steps = ((tiles + shares - 1) / shares + 7) / 8;  // of a wave, for each tile of keys
+            shares = (tiles + 8 * steps - 1) / (8 * steps);                 // the fewest for that
             const double us = double((pairs * shares + kUnits - 1) / kUnits) *
-                              (5.0 + double((per + 7) / 8) * double(kt) * 2.3);
+                              (5.0 + double(steps) * double(kt) * 2.3);
             if (us >= best) continue;
             best = us;
             p.kernel = Kernel::near;

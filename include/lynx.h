@@ -430,19 +430,21 @@ lynx_status lynx_qk_rotary(const lynx_rotary* rotary, lynx_stream_t stream);
  * already holds their own keys).  With a prefix (prefix_tokens > 0), every query of every
  * sequence also sees all prefix keys, which come before the sequence's own; causal
  * concerns own keys alone.  A query that sees no key gets out = 0 and lse = -infinity.
- *   - Scores and sums are fp32.  p_j is rounded to bf16 for its product with v_j (not
- *     for the sum), taken relative to a power of two no further than 2^9 below the
- *     row's largest; out has one more rounding.  A row's result does not depend on what other
- *     rows hold, and is the same in every call of the same sizes, offsets and strides.
+ *   - Scores and sums are fp32.  p_j, taken relative to a power of two no further than 2^9
+ *     below the row's largest, is rounded to bf16, for its product with v_j and for out's
+ *     divisor alike (lse sums the p_j before that); out has one more rounding.  A row's
+ *     result does not depend on what other rows hold, and is the same in every call of the
+ *     same sizes, offsets and strides.
  *   - Keys that a query does not see have no influence on it, whatever they hold; with
  *     NaN or infinities among the keys and values that it sees, its row is as the
  *     formula gives it (an infinite or NaN value whose p_j is 0 makes NaN), and so with a
- *     score that passes fp32's range.
+ *     score that passes fp32's range; but scores that are all -infinity count as no key seen.
  *   - Rows of out and lse before cu_q[0] and from cu_q[batch] on are left as they were.
- *     Offsets must not decrease and lie within 0 .. tokens_q (tokens_k); the device checks this only
- *     so far that no other call's memory is touched: results of other offsets are unspecified.
+ *     Offsets must not decrease and lie within 0 .. tokens_q (tokens_k); the device checks
+ *     this only so far that no memory beside the tensors is touched: results of other offsets
+ *     are unspecified.
  *   - Strides are in elements, multiples of 8, not negative; channels are contiguous.
- *     Token strides of k, v and the prefix are at least head_dim and below 2^24.  Heads
+ *     Token strides of k, v and the prefix are at least head_dim and below 2^23.  Heads
  *     may share memory (head stride 0) in inputs.  out overlaps no input, and its rows
  *     do not overlap.
  *   - Sequences of any length may be mixed.  Which kernel runs, and whether keys are
@@ -450,9 +452,9 @@ lynx_status lynx_qk_rotary(const lynx_rotary* rotary, lynx_stream_t stream);
  *     are alike in length are the fastest.
  * Limits: head_dim a multiple of 8, 8..128; 1 <= kv_heads, heads a multiple of it, <= 1024;
  * 1 <= batch <= 2^16; tokens_q, tokens_k and prefix_tokens each 0..2^26 (tokens_q == 0
- * is a no-op), in the uniform form multiples of batch; tokens_q * heads < 2^30; scale > 0
- * and finite.  q, k, v, out and prefix pointers are 16-byte aligned, cu_* and lse 4-byte.  k and v may be NULL
- * if tokens_k is 0.
+ * is a no-op), in the uniform form multiples of batch; tokens_q * heads < 2^30; batch *
+ * kv_heads <= 2^21; scale > 0 and finite.  q, k, v, out and prefix pointers are 16-byte
+ * aligned, cu_* and lse 4-byte.  k and v may be NULL if tokens_k is 0.
  */
 typedef struct lynx_attn {
     const uint16_t* q;        /* bf16 */
@@ -476,9 +478,9 @@ typedef struct lynx_attn {
 } lynx_attn;
 
 /*
- * Bytes of device workspace lynx_attention needs for these sizes (pointers and strides
- * are not looked at, except whether prefix_tokens is 0); 0 where it needs none, and for
- * invalid sizes.  Contents on entry irrelevant, clobbered; 256-byte aligned; NULL is
+ * Bytes of device workspace lynx_attention needs for these sizes, causal or not, and
+ * offsets given (cu_q not NULL) or not; nothing else is looked at.  0 where it needs none, and
+ * for invalid sizes.  Contents on entry irrelevant, clobbered; 256-byte aligned; NULL is
  * allowed where it is 0.  Calls that may overlap need workspaces of their own.
  */
 size_t lynx_attention_workspace_bytes(const lynx_attn* attn);

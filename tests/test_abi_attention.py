@@ -69,7 +69,8 @@ def attn(ws=None, n=0, **kw):
     (dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=NAN), SHAPE), (dict(scale=INF), SHAPE),
     (dict(q_stride=4), SHAPE), (dict(k_stride=-8), SHAPE), (dict(out_head_stride=1), SHAPE),
     (dict(q_batch_stride=7), SHAPE), (dict(k_stride=56), SHAPE), (dict(v_stride=0), SHAPE),
-    (dict(k_stride=1 << 24), SHAPE), (PREFIX | dict(prefix_v_stride=0), SHAPE),
+    (dict(k_stride=1 << 24), SHAPE), (dict(v_stride=1 << 23), SHAPE),
+    (dict(batch=1 << 16, tokens_q=1 << 16, heads=64, kv_heads=64), SHAPE), (PREFIX | dict(prefix_v_stride=0), SHAPE),
     (PREFIX | dict(prefix_k_head_stride=4), SHAPE),
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(out=None), NULL),
     (dict(cu_q=A), NULL), (dict(cu_k=A), NULL), (dict(prefix_k=A), NULL), (PREFIX | dict(prefix_v=None), NULL),
@@ -95,6 +96,8 @@ def test_attention_workspace():
     assert f(1, 1, 9000, 1, 1, 64) > 0
     assert f(4, 4, 4, 1, 1, 64, prefix_tokens=1) > 0   # a prefix of its own is joined
     assert f(0, 4, 4, 1, 1, 64) == 0 and f(1, 4, 4, 3, 2, 64) == 0 and f(1, 4, 4, 1, 1, 60) == 0
+    sizes = (1, 64, 1 << 17, 8, 8, 128)                # as the call is: causal ones are cut otherwise
+    assert all(f(*sizes, causal=c) > 0 for c in (False, True))
     for packed in (False, True):                       # never past a GiB for the sake of uneven lengths
         for tq, tk in ((1, 1 << 26), (64, 1 << 20), (4096, 1 << 20), (1 << 16, 1 << 20)):
             assert f(1, tq, tk, 32, 8, 128, packed=packed) <= 1 << 30

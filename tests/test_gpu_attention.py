@@ -59,10 +59,10 @@ def check(out, lse, ref, D, n):
         assert (np.abs(gl[~empty] - l[~empty]) <= tl[~empty]).all()
 
 
-def poisoned(q, B, Tk, kv, P, packed, shape=None):
+def poisoned(q, B, Tk, kv, P, packed, causal):
     """out, lse and workspace that hold what no call may read or leave."""
     Tq = q.numel() // (q.shape[-1] * q.shape[-2])
-    n = lynx.attention_workspace_bytes(B, Tq, Tk, q.shape[-2], kv, q.shape[-1], P, packed)
+    n = lynx.attention_workspace_bytes(B, Tq, Tk, q.shape[-2], kv, q.shape[-1], P, packed, causal)
     return dict(out=nan_bf16(tuple(q.shape)),
                 lse=torch.full(q.shape[:-1], NAN, device="cuda"), workspace=poisoned_bytes(n))
 
@@ -75,7 +75,7 @@ def packed_case(lens_q, lens_k, heads, kv, D, causal, seed, P=0, scale=None, siz
                        tuple(map(host_f64, prefix)) if P else None)
     say(f"packed q={lens_q[:8]} k={lens_k[:8]} n={len(lens_q)} {heads}/{kv}x{D} causal={causal} P={P}")
     out, lse = lynx.attention(q, k, v, offsets(lens_q), offsets(lens_k), causal, scale, prefix,
-                              **poisoned(q, len(lens_q), sum(lens_k), kv, P, True))
+                              **poisoned(q, len(lens_q), sum(lens_k), kv, P, True, causal))
     torch.cuda.synchronize()
     check(out, lse, ref, D, max(lens_k) + P)
     return out, lse
@@ -176,7 +176,7 @@ def test_uniform_batches_and_strides(B, Lq, Lk, heads, kv, D, causal, layout):
     ref = ao.attention(*(host_f64(t).reshape(-1, t.shape[2], D) for t in (q, k, v)), [Lq] * B, [Lk] * B,
                        causal)
     say(f"uniform {layout} {B}x{Lq}x{Lk} {heads}/{kv}x{D} causal={causal}")
-    kw = poisoned(q, B, B * Lk, kv, 0, False)
+    kw = poisoned(q, B, B * Lk, kv, 0, False, causal)
     if layout == "BHSD":
         kw["out"] = nan_bf16((B, heads, Lq, D)).transpose(1, 2)
     out, lse = lynx.attention(q, k, v, causal=causal, **kw)
@@ -199,7 +199,7 @@ def test_many_rows_on_few_keys(B, Lq, Lk, heads, kv, D, layout):
     ref = ao.attention(host_f64(q[:, some]).reshape(-1, heads, D),
                        *(host_f64(t).reshape(-1, kv, D) for t in (k, v)), [len(some)] * B, [Lk] * B, False)
     say(f"few keys {layout} {B}x{Lq}x{Lk} {heads}/{kv}x{D}")
-    kw = poisoned(q, B, B * Lk, kv, 0, False)
+    kw = poisoned(q, B, B * Lk, kv, 0, False, False)
     if layout == "BHSD":
         kw["out"] = nan_bf16((B, heads, Lq, D)).transpose(1, 2)
     out, lse = lynx.attention(q, k, v, **kw)
@@ -359,6 +359,20 @@ def test_a_cache_of_more_than_4_gib():
     check(out, lse, ref, D, 300)
 
 
+@pytest.mark.parametrize("lq,D", [(140, 56), (140, 104), (3, 56)])
+def test_the_largest_token_stride(lq, D):
+    """Keys nearly 16 MiB apart: a tile of them spans nearly 2^31 bytes, and the channels behind
+    head_dim, which count as zero, hold NaN here."""
+    stride, lk = (1 << 23) - 8, 130
+    memory = torch.full((lk * stride,), NAN, dtype=torch.bfloat16, device="cuda")
+    k, v = (memory[at:].as_strided((lk, 1, D), (stride, D, 1)) for at in (0, 512))
+    k.copy_(randn((lk, 1, D), 1))
+    v.copy_(randn((lk, 1, D), 2))
+    q = randn((lq, 1, D), 3)
+    out, lse = lynx.attention(q, k, v, return_lse=True)
+    check(out, lse, ao.attention(host_f64(q), host_f64(k), host_f64(v), [lq], [lk]), D, lk)
+
+
 # ---- calls ------------------------------------------------------------------------
 
 CALLS = {
@@ -383,7 +397,7 @@ def test_the_same_bytes_every_time(name):
     ref = lynx.attention(return_lse=True, **t)
     lq, lk, heads, kv, D, P = CALLS[name]
     for _ in range(3):
-        got = lynx.attention(**t, **poisoned(t["q"], len(lq), sum(lk), kv, P, True))
+        got = lynx.attention(**t, **poisoned(t["q"], len(lq), sum(lk), kv, P, True, True))
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
