@@ -25,7 +25,7 @@ constexpr int kNearTiles = 5;    // of keys, that the kernel for few keys has ro
 // Keys are cut into tiles (the prefix' tiles first, then the sequence's own), tiles into
 // chunks of at least chunk_tiles, at most chunk_max of them to a sequence.  Work is the list
 // of (sequence, key head, row tile, chunk).  Where slots > 0 a chunk's result goes to the
-// partial sums: row's slot slot0 + chunk, part_n[row] chunks; lynx_attn_join adds them up.  A
+// partial sums: row's slot slot0 + chunk, part_n[row] chunks; attn_join_kernel adds them up.  A
 // sequence of one chunk goes straight to out, unless force_part.
 struct AttnArgs {
     const uint16_t *q, *k, *v, *pk, *pv;
