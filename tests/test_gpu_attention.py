@@ -121,6 +121,16 @@ def test_many_sequences(lens_q, causal):
     packed_case([lens_q] * 150, [max(n, lens_q) for n in lk], 4, 2, 64, causal, 50 + lens_q)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_one_long_sequence_among_single_tokens(D, causal):
+    # the long one has 38 row tiles of 32, and several chunks of keys
+    n = 60
+    lens_q, lens_k = [1] * n + [300] + [1] * n, list(range(1, 7 * n, 7)) + [4000] + [33] * n
+    packed_case(lens_q, lens_k, 4, 1, D, causal, 5)
+    packed_case(lens_q, lens_k, 4, 1, D, causal, 9, P=700)
+
+
 @pytest.mark.parametrize("lq,lk,heads,kv,D", [
     (1, 1, 1, 1, 128), (1, 9000, 8, 1, 128), (4, 5001, 8, 8, 64), (33, 4100, 1, 1, 128),
     (100, 6000, 2, 2, 128), (200, 3001, 4, 1, 72), (1, 700, 64, 1, 128), (700, 40, 2, 1, 128),
