@@ -104,9 +104,10 @@ struct AttnPlan {
 // The piece of work of workgroup `block`; false if there is none.  Uniform over the workgroup.
 // Workgroups of one XCD (their number mod 8) take the same key heads, one after the other, so that
 // its L2 holds the keys and values that its workgroups read; where there are fewer key heads than
-// XCDs several share a head.  Within a head sequences follow one another, and a sequence's row tiles
-// come last tile first: under a causal mask these have the most keys, and the light ones fill the
-// end.
+// XCDs several share a head.  Within a head sequences follow one another, those of most keys first
+// where there are up to 64 (12 of 32 .. 4096 causal tokens, 32/8 x 128: 135 -> 130 us; not for few
+// rows, whose pieces are of one size), and a sequence's row tiles come last tile first: under a causal mask these have the most keys, and the light ones fill
+// the end.
 template <int BM, int BN>
 __device__ __forceinline__ bool attn_item(const AttnArgs& A, int block, AttnItem& w) {
     const int lane = threadIdx.x & 63;
@@ -129,11 +130,29 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& A, int block, AttnItem
     const int xcd = block & 7, slot = block >> 3, share = 8 / A.classes;
     const int idx = slot * share + xcd / A.classes;
     Range mine = {0, 0, 0, 0};
+    int seq = lane;   // whose range that is, behind `base`
     int per_head, sum = 0;  // pieces to a key head; of the sequences up to this lane's (the first 64)
     if (A.cu_q) {
         if (lane < A.batch) {
             mine = range(lane);
             sum = pieces(mine);
+        }
+        if (BM > 32 && A.batch <= 64) {
+            int rank = lane;
+            if (lane < A.batch) {
+                rank = 0;
+                for (int i = 0; i < A.batch; ++i) {
+                    const int other = __builtin_amdgcn_readlane(mine.lk, i);
+                    rank += other > mine.lk || (other == mine.lk && i < lane);
+                }
+            }
+            auto move = [&](int& v) { v = __builtin_amdgcn_ds_permute(rank * 4, v); };
+            move(mine.q0);
+            move(mine.lq);
+            move(mine.k0);
+            move(mine.lk);
+            move(sum);
+            move(seq);
         }
         sum = wave_scan(sum, lane, A.batch);
         per_head = __builtin_amdgcn_readlane(sum, min(A.batch, 64) - 1);
@@ -168,7 +187,7 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& A, int block, AttnItem
         const int l = __builtin_ctzll(over);
         if (l > 0) before += __builtin_amdgcn_readlane(sum, l - 1);
         r = sgpr(r - before);
-        w.seq = base + l;
+        w.seq = base + __builtin_amdgcn_readlane(seq, l);
         w.q0 = __builtin_amdgcn_readlane(mine.q0, l);
         w.lq = __builtin_amdgcn_readlane(mine.lq, l);
         w.k0 = __builtin_amdgcn_readlane(mine.k0, l);

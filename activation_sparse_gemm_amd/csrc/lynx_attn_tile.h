@@ -8,7 +8,7 @@
 //
 // The matrix unit's and the vector unit's time together bound it: two waves of a SIMD take 3700
 // cycles for a step each (128 channels), of which products fill 2112.  4 x 1024 queries on a prefix of 2560 and their
-// own keys, 24 x 128: 187 us, 970 TFLOP/s; 8661 tokens in 7 causal sequences, 32/8 x 128: 236 us, 850.
+// own keys, 24 x 128: 187 us, 970 TFLOP/s; 8661 tokens in 7 causal sequences, 32/8 x 128: 235 us, 855.
 #pragma once
 
 #include "lynx_attn_wave.h"
