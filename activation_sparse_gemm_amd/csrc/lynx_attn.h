@@ -106,8 +106,8 @@ struct AttnPlan {
 // its L2 holds the keys and values that its workgroups read; where there are fewer key heads than
 // XCDs several share a head.  Within a head sequences follow one another, those of most keys first
 // where there are up to 64 (12 of 32 .. 4096 causal tokens, 32/8 x 128: 135 -> 130 us; not for few
-// rows, whose pieces are of one size), and a sequence's row tiles come last tile first: under a causal mask these have the most keys, and the light ones fill
-// the end.
+// rows, whose pieces are of one size), and a sequence's row tiles come last tile first: under a
+// causal mask these have the most keys, and the light ones fill the end.
 template <int BM, int BN>
 __device__ __forceinline__ bool attn_item(const AttnArgs& A, int block, AttnItem& w) {
     const int lane = threadIdx.x & 63;

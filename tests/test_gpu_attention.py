@@ -121,6 +121,15 @@ def test_many_sequences(lens_q, causal):
     packed_case([lens_q] * 150, [max(n, lens_q) for n in lk], 4, 2, 64, causal, 50 + lens_q)
 
 
+@pytest.mark.parametrize("n", [2, 63, 64, 65, 130])
+@pytest.mark.parametrize("causal", [False, True])
+def test_row_tiles_of_many_sequences(n, causal):
+    # lengths that rise and fall, some of them alike, some zero
+    lens = [(37 * i) % 90 * (i % 5 != 3) + 20 * (i % 7 == 0) for i in range(n)]
+    packed_case(lens, [a + (i * 11) % 50 for i, a in enumerate(lens)], 4, 2, 64, causal, 3)
+    packed_case(lens, lens, 2, 2, 128, causal, 4, P=65)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("causal", [False, True])
 def test_one_long_sequence_among_single_tokens(D, causal):
