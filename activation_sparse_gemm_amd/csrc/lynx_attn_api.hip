@@ -122,6 +122,25 @@ struct Plan {
 
 constexpr int kUnits = 256;
 
+// Row tiles and chunks that the kernel of pass p makes of a sequence of lq queries and lk keys; as its
+// workgroups work them out.
+struct Cut {
+    int tiles, chunks;
+};
+Cut cut_of(const Pass& p, int group, int prefix, int64_t D, int lq, int lk) {
+    AttnArgs a = {};
+    a.group = group;
+    a.prefix = prefix;
+    a.chunk_tiles = p.chunk_tiles;
+    a.chunk_max = p.chunk_max;
+    auto of = [](auto plan) { return Cut{plan.tiles, plan.chunks}; };
+    const bool small = D <= 64;  // (tiles of keys are 128 then)
+    if (p.kernel == Kernel::few) return of(AttnPlan<32, 128>(a, lq, lk));
+    if (p.kernel == Kernel::tile)
+        return small ? of(AttnPlan<128, 128>(a, lq, lk)) : of(AttnPlan<128, 64>(a, lq, lk));
+    return small ? of(AttnPlan<256, 128>(a, lq, lk)) : of(AttnPlan<256, 64>(a, lq, lk));
+}
+
 // Which kernel takes a pass, and into how many chunks it cuts the keys.  rows: query rows to a
 // key head, over all sequences; keys: of all sequences together; shared: keys that each sequence has
 // besides; seen: the share of the keys that a mask leaves; joined: whether the join runs anyway;
@@ -250,6 +269,10 @@ Plan make_plan(const lynx_attn& d, bool ragged) {
     if (P.apart) {
         const int64_t pairs = P.own.kernel == Kernel::few ? d.batch * d.kv_heads : 0;
         P.prefix = plan_pass(1, rows, d.prefix_tokens, 0, d.kv_heads, d.head_dim, false, 1.0, true, pairs);
+        // The join reads as many slots of every row as this says, so it has to be what is written:
+        // 547 tiles in at most 128 chunks are 110 of 5.
+        P.prefix.chunk_max =
+            cut_of(P.prefix, int(group), 0, d.head_dim, int(d.tokens_q), int(d.prefix_tokens)).chunks;
         slots = P.own.chunk_max + P.prefix.chunk_max;
     }
     P.slots = slots;
@@ -349,15 +372,8 @@ lynx_status lynx_attention(const lynx_attn* attn, void* workspace, size_t worksp
     auto cut = [&](AttnArgs& args, const Pass& p) {
         args.chunk_tiles = p.chunk_tiles;
         args.chunk_max = p.chunk_max;
-        auto pieces = [&](auto plan) { return plan.tiles * plan.chunks; };
-        const bool small = args.D <= 64;  // (tiles of keys are 128 then)
-        args.pieces = p.kernel == Kernel::near  ? p.shares
-                      : p.kernel == Kernel::few ? pieces(AttnPlan<32, 128>(args, args.len_q, args.len_k))
-                      : p.kernel == Kernel::tile
-                          ? (small ? pieces(AttnPlan<128, 128>(args, args.len_q, args.len_k))
-                                   : pieces(AttnPlan<128, 64>(args, args.len_q, args.len_k)))
-                          : (small ? pieces(AttnPlan<256, 128>(args, args.len_q, args.len_k))
-                                   : pieces(AttnPlan<256, 64>(args, args.len_q, args.len_k)));
+        const Cut c = cut_of(p, args.group, args.prefix, args.D, args.len_q, args.len_k);
+        args.pieces = p.kernel == Kernel::near ? p.shares : c.tiles * c.chunks;
     };
     auto run = [&](const AttnArgs& args, const Pass& p) {
         switch (p.kernel) {

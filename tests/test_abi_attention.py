@@ -103,6 +103,16 @@ def test_attention_workspace():
             assert f(1, tq, tk, 32, 8, 128, packed=packed) <= 1 << 30
 
 
+def test_a_row_has_as_many_partial_results_as_pieces_of_the_prefix():
+    # 70000 keys are 547 tiles of 128; at most 128 pieces of whole tiles are 110 of 5, and the
+    # tokens' own keys are one more.  What is not written must not be there to be joined.
+    rows, slots, D = 2 * 8, 110 + 1, 128
+    up = lambda n: (n + 255) // 256 * 256
+    want = up(rows * slots * D * 4) + up(rows * slots * 16) + up(rows * 4)
+    for packed in (False, True):
+        assert lynx.attention_workspace_bytes(2, 2, 20, 8, 1, D, 70000, packed, True) == want
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="valid fake pointers must not reach a launch")
 def test_valid_arguments_reach_the_device_check():
     assert rotary() == UNSUPPORTED

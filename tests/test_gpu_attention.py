@@ -160,6 +160,17 @@ def test_shared_prefix(lens_q, lens_k, P, heads, kv, D, causal):
     packed_case(lens_q, lens_k, heads, kv, D, causal, 70 + P, P)
 
 
+@pytest.mark.parametrize("lens_q,lens_k,heads,kv,P", [
+    ([1, 1], [9, 11], 8, 1, 70000), ([1] * 4, [5, 0, 300, 1], 12, 2, 100000), ([1, 2], [30, 2], 8, 2, 84489),
+    ([3, 0, 1], [3, 7, 1], 3, 3, 96488), ([1] * 4, [5, 0, 300, 1], 12, 2, 65536),
+])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_long_prefix_of_few_key_heads(lens_q, lens_k, heads, kv, P, D):
+    """The prefix is cut into the most pieces that there are, or, since pieces are of whole tiles,
+    fewer: the join reads no others (the workspace holds NaN)."""
+    packed_case(lens_q, lens_k, heads, kv, D, True, 90 + kv, P)
+
+
 def test_the_prefix_is_the_keys_before():
     """The same keys as a prefix and as each sequence's own give the same result, up to rounding."""
     lens, P = [3, 50, 129], 200
