@@ -71,7 +71,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& A, int block, char* sme
         W.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         wait_vmcnt<(2 * RING - 1) * PER>();  // V(t)
         asm volatile("" ::: "memory");
-        if (CAUSAL && !pre && view.all < view.any && key0 + 32 > view.all) {
+        if (CAUSAL && !pre && view.all < view.lk && key0 + 32 > view.all) {
             W.multiply_hidden(smem, va + at, view.seen - key0);
         } else {
             W.template ahead<false, true>(smem, ka + at, va + at);

@@ -326,8 +326,8 @@ struct AttnTile : AttnWave<DP, LSE> {
     __device__ __forceinline__ static uint32_t odd_halves(uint32_t w) {
         return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
     }
-    // O^T += V^T P^T where rows differ in the keys they see (left: how many of the tile's a lane's
-    // row does).  A hidden key's weight is 0, but its value may be infinite or NaN, and 0 times
+    // O^T += V^T P^T where rows do not see every key (left: how many of the tile's a lane's row
+    // does).  A hidden key's weight is 0, but its value may be infinite or NaN, and 0 times
     // that is NaN: such values are taken as 0, and added, key by key, to the rows that see them.
     __device__ __forceinline__ void multiply_hidden(const char* smem, uint32_t v, int left) {
         typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -476,10 +476,10 @@ __device__ __forceinline__ void open_stream(S& s, const AttnArgs& A, const AttnI
     s.open(span, A.prefix, w.lk, base, t, pbase, pt, first, A.D, lds, wave, lane);
 }
 
-// What a wave's rows see of the sequence's own keys: a lane's row `seen`, all of them `all`, any
+// What a wave's rows see of the sequence's own lk keys: a lane's row `seen`, all of them `all`, any
 // of them `any`.  none: the wave has no row.
 struct AttnView {
-    int seen, all, any;
+    int seen, all, any, lk;
     bool none;
     __device__ __forceinline__ AttnView(const AttnArgs& A, const AttnItem& w, int row0, int lane) {
         auto keys = [&](int t) { return A.causal ? clampi(t + w.lk - w.lq + 1, 0, w.lk) : w.lk; };
@@ -487,12 +487,14 @@ struct AttnView {
         seen = keys(row_token(A, row0 + (lane & 31)));
         all = keys(t0);
         any = keys(t1);
+        lk = w.lk;
         none = t0 >= w.lq;
     }
-    // of these, the first ones of which the rows see the same keys
+    // of these, the first ones of which all rows see every key.  (Not: of which they see the same keys.
+    // 32 rows of one token do, and their last tile still holds the keys of later tokens.)
     template <int BMR, int BN>
     __device__ __forceinline__ int plain(const AttnSpan<BMR, BN>& span) const {
-        return all < any ? clampi(span.tp + all / BN - span.j0, 0, span.n) : span.n;
+        return all < lk ? clampi(span.tp + all / BN - span.j0, 0, span.n) : span.n;
     }
     // the item's tiles that the wave works on: the first ones
     template <int BMR, int BN>

@@ -365,6 +365,36 @@ def test_keys_that_are_hidden_may_hold_anything(lq, lk, heads, kv, D, P):
         assert torch.isnan(out[i:]).all() and torch.isnan(lse[i:]).all()
 
 
+@pytest.mark.parametrize("lq,lk,heads,kv", [(130, 200, 32, 1), (77, 333, 40, 1), (45, 130, 71, 1), (300, 300, 64, 2),
+                                            (2000, 2000, 64, 2)])
+@pytest.mark.parametrize("D,P", [(64, 0), (128, 40)])
+def test_hidden_keys_of_rows_of_one_token(lq, lk, heads, kv, D, P):
+    """With 32 heads to a key head and more all rows of a wave may be of one token, which see the same
+    keys, and still not all keys of a tile.  (The last: 256-row tiles.)"""
+    test_keys_that_are_hidden_may_hold_anything(lq, lk, heads, kv, D, P)
+
+
+@pytest.mark.parametrize("heads", [32, 40, 71])
+@pytest.mark.parametrize("D", [64, 72, 128])
+def test_hidden_keys_of_few_rows_of_one_token(heads, D):
+    """The same in the few-row kernel: its row tiles by the mean of sequences that have no queries too."""
+    lens_q, lens_k = [2] + [0] * 12 + [3], [150, 0, 9, 1] + [0] * 9 + [33]
+    q, k, v = randn((5, heads, D), 1), randn((193, 1, D), 2), randn((193, 1, D), 3)
+    kw = dict(cu_q=offsets(lens_q), cu_k=offsets(lens_k), causal=True)
+    want = lynx.attention(q, k, v, **kw)
+    say(f"hidden keys of few rows {heads}/1x{D}")
+    for key, first in ((149, 1), (191, 3), (192, 4)):  # the first row that sees the key
+        seen = 2 if first < 2 else 5                   # and the first after it that does not
+        a = v.clone()
+        a[key, :, 3], a[key, :, 5] = INF, NAN
+        out = lynx.attention(q, k, a, **kw)
+        others = [i for i in range(5) if not first <= i < seen]
+        assert torch.equal(out[others], want[others])
+        assert torch.isnan(out[first:seen, :, 5]).all() and not torch.isfinite(out[first:seen, :, 3]).any()
+        rest = [c for c in range(D) if c not in (3, 5)]
+        assert torch.equal(out[..., rest], want[..., rest])
+
+
 # ---- offsets past 32 bits ----------------------------------------------------------
 
 def test_a_cache_of_more_than_4_gib():
