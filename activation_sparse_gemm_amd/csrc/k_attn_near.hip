@@ -57,7 +57,7 @@ __global__ __launch_bounds__(512, 2) void attn_near_kernel(const AttnArgs A) {
     const uint32_t ka = W.k_first(), va = W.v_first() + RING * TILE;
     auto weigh = [&](int t) {
         if ((t + 1) * BN > w.lk) W.hide(t * BN, w.lk);
-        W.raise(W.maximum(W.s, A.c));
+        W.relate(W.maximum(W.s, A.c), A.c);
         float sum[4] = {W.l, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < W.NB; ++b) W.weights(W.s[b], A.c, W.p[b], sum);

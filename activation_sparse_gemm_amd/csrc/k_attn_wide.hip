@@ -83,7 +83,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs A) {
         load(ks, 0);
         const float top = W.maximum(W.s, A.c);
         load(ks, 1);
-        W.raise(top);
+        W.relate(top, A.c);
         float sum[4] = {W.l, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < W.NB; ++b) {

@@ -65,7 +65,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& A, int block, char* sme
         const int j = span.j0 + t, key0 = span.key(j) + 32 * wave;
         const bool pre = j < span.tp;
         if (key0 + 32 > (pre ? A.prefix : view.all)) W.hide(key0, pre ? A.prefix : view.seen);
-        W.raise(W.maximum(W.s, A.c));
+        W.relate(W.maximum(W.s, A.c), A.c);
         float sum[4] = {W.l, 0.f, 0.f, 0.f};
         W.weights(W.s[0], A.c, W.p[0], sum);
         W.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);

@@ -49,7 +49,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& A, int block, char* sm
         const int j = span.j0 + t, key0 = span.key(j);
         const bool pre = j < span.tp;
         if (key0 + BN > (pre ? A.prefix : view.all)) W.hide(key0, pre ? A.prefix : view.seen);
-        W.raise(W.maximum(W.s, A.c));
+        W.relate(W.maximum(W.s, A.c), A.c);
         float sum[4] = {W.l, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < W.NB; ++b) W.weights(W.s[b], A.c, W.p[b], sum);

@@ -243,13 +243,22 @@ struct AttnWave {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[d][e] *= f;
     }
+    // Lanes whose row's |m| may be 2^24 or more after raise(top).  (Where m is below -2^24 and top is not,
+    // m is raised.)
+    __device__ __forceinline__ uint64_t far(float top) const { return __ballot(fmaxf(fabsf(top), m) >= 16777216.f); }
+    __device__ __forceinline__ bool near() const { return fabsf(m) < 16777216.f; }
+    __device__ __forceinline__ static float apart(float v, float c, float from) {
+#pragma clang fp contract(off)
+        const float t = v * c;
+        return t - from;
+    }
 
     // Scores of 32 keys to weights, P^T's operand for two steps of 16 keys, and their sums: two
     // partial sums to a step, since a chain's step takes longer.
     __device__ __forceinline__ void weights(f32x16& s, float c, u32x4 (&p)[2], float (&sum)[4]) {
         typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
         const bf16x2 one = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
-        const float base = m == -INFINITY ? 0.f : m;
+        const float base = near() ? m : 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -base));
@@ -387,6 +396,23 @@ struct AttnTile : AttnWave<DP, LSE> {
 #pragma unroll
             for (int e = 0; e < 16; ++e) W::o[d][e] += sees ? c[e] : 0.f;
         }
+    }
+    // Raises m to a tile's scores, before their weights.  A multiply-add takes c s as it is, and m is
+    // fp32: from 2^24 on, c s - m of a row's largest score is what m has lost, up to half its last
+    // place, which passes 2^7 from 2^31 on (weights of infinity, or of 0 alone).  In such rows c s is
+    // rounded as m was, and the scores become those that are as far from 0 as c s was from m.
+    __device__ __forceinline__ void relate(float top, float c) {
+        // (early, since a branch waits for its condition: 16384 x 16384 x 8 heads 980 us without, 993 so,
+        // 998 with the condition after m is raised)
+        const uint64_t rows = W::far(top);
+        W::raise(top);
+        if (rows == 0) return;
+        const bool mine = !W::near() && W::m != -INFINITY;
+        const float back = 1.f / c;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[b][e] = mine ? W::apart(s[b][e], c, W::m) * back : s[b][e];
     }
     // Hides keys from `seen` on; key0: the tile's first
     __device__ __forceinline__ void hide(int key0, int seen) {
