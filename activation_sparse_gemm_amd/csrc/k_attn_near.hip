@@ -58,10 +58,10 @@ __global__ __launch_bounds__(512, 2) void attn_near_kernel(const AttnArgs A) {
     auto weigh = [&](int t) {
         if ((t + 1) * BN > w.lk) W.hide(t * BN, w.lk);
         W.relate(W.maximum(W.s, A.c), A.c);
-        float sum[4] = {W.l, 0.f, 0.f, 0.f};
+        typename decltype(W)::Sums sum;
 #pragma unroll
         for (int b = 0; b < W.NB; ++b) W.weights(W.s[b], A.c, W.p[b], sum);
-        W.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        W.add(sum);
     };
     wait_vmcnt<0>();
     block_barrier();

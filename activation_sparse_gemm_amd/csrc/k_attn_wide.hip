@@ -84,13 +84,13 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnArgs A) {
         const float top = W.maximum(W.s, A.c);
         load(ks, 1);
         W.relate(top, A.c);
-        float sum[4] = {W.l, 0.f, 0.f, 0.f};
+        typename decltype(W)::Sums sum;
 #pragma unroll
         for (int b = 0; b < W.NB; ++b) {
             W.weights(W.s[b], A.c, W.p[b], sum);
             if (b % (W.NB / 2) == 0) load(vs, b / (W.NB / 2));
         }
-        W.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        W.add(sum);
         // here, not after the barrier: its only use is far away
         asm volatile("" : "+v"(W.l));
     };

@@ -66,9 +66,9 @@ __device__ __forceinline__ void attn_few(const AttnArgs& A, int block, char* sme
         const bool pre = j < span.tp;
         if (key0 + 32 > (pre ? A.prefix : view.all)) W.hide(key0, pre ? A.prefix : view.seen);
         W.relate(W.maximum(W.s, A.c), A.c);
-        float sum[4] = {W.l, 0.f, 0.f, 0.f};
+        typename decltype(W)::Sums sum;
         W.weights(W.s[0], A.c, W.p[0], sum);
-        W.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        W.add(sum);
         wait_vmcnt<(2 * RING - 1) * PER>();  // V(t)
         asm volatile("" ::: "memory");
         if (CAUSAL && !pre && view.all < view.lk && key0 + 32 > view.all) {

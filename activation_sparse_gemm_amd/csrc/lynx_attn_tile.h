@@ -50,10 +50,10 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& A, int block, char* sm
         const bool pre = j < span.tp;
         if (key0 + BN > (pre ? A.prefix : view.all)) W.hide(key0, pre ? A.prefix : view.seen);
         W.relate(W.maximum(W.s, A.c), A.c);
-        float sum[4] = {W.l, 0.f, 0.f, 0.f};
+        typename decltype(W)::Sums sum;
 #pragma unroll
         for (int b = 0; b < W.NB; ++b) W.weights(W.s[b], A.c, W.p[b], sum);
-        W.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        W.add(sum);
     };
 
     // K(0), and q: where the compiler knows of loads of q under way it waits for all loads

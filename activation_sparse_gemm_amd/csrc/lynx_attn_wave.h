@@ -142,8 +142,8 @@ struct AttnWave {
     f32x16 o[DB];
     // m: a whole power of two, -inf before the first key that is seen; l: the sum of the
     // weights as the product with V takes them, rounded to bf16, so that a row on which one key
-    // dominates is not off by that key's rounding; exact: of the weights before it, for lse
-    float m, l, exact;
+    // dominates is not off by that key's rounding; exact - lost: of the weights before it, for lse
+    float m, l, exact, lost;
     int lane, h;
 
     // p: the lane's query row, or NULL
@@ -155,7 +155,7 @@ struct AttnWave {
     }
     __device__ __forceinline__ void clear() {
         m = -INFINITY;
-        l = exact = 0.f;
+        l = exact = lost = 0.f;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -238,6 +238,7 @@ struct AttnWave {
         m = to;
         l *= f;
         exact *= f;
+        lost *= f;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -253,22 +254,36 @@ struct AttnWave {
         return t - from;
     }
 
-    // Scores of 32 keys to weights, P^T's operand for two steps of 16 keys, and their sums: two
-    // partial sums to a step, since a chain's step takes longer.
-    __device__ __forceinline__ void weights(f32x16& s, float c, u32x4 (&p)[2], float (&sum)[4]) {
+    // A tile's sums of weights, in four parts, since a chain's step takes longer.
+    struct Sums {
+        float rounded[4] = {0.f, 0.f, 0.f, 0.f}, exact[4] = {0.f, 0.f, 0.f, 0.f};
+    };
+    // Scores of 32 keys to weights, P^T's operand for two steps of 16 keys, and their sums
+    __device__ __forceinline__ void weights(f32x16& s, float c, u32x4 (&p)[2], Sums& sum) {
         typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
         const bf16x2 one = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
         const float base = near() ? m : 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -base));
-            if constexpr (LSE) exact += s[e];
-        }
+        for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -base));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t w = pack_bf16(s[2 * i], s[2 * i + 1]);
-            sum[i % 4] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, sum[i % 4], false);
+            sum.rounded[i % 4] =
+                __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, sum.rounded[i % 4], false);
+            if constexpr (LSE) sum.exact[i % 4] += s[2 * i] + s[2 * i + 1];
             p[i / 4][i % 4] = w;
+        }
+    }
+    // A tile's sums to the row's: once a tile, since weights that are alike all round the same way in a
+    // sum that has grown.  lse's sum keeps what such an addition loses (Kahan), so that its error does
+    // not grow with the keys: lse of 262144 equal scores was 2e-3 off with every weight added singly, and is
+    // 2e-6 off so.  (l goes with o, which the matrix instructions sum in fp32, 16 keys at a time.)
+    __device__ __forceinline__ void add(const Sums& t) {
+        l += (t.rounded[0] + t.rounded[1]) + (t.rounded[2] + t.rounded[3]);
+        if constexpr (LSE) {
+            const float y = ((t.exact[0] + t.exact[1]) + (t.exact[2] + t.exact[3])) - lost, n = exact + y;
+            lost = (n - exact) - y;
+            exact = n;
         }
     }
 };

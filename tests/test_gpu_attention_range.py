@@ -65,3 +65,31 @@ def test_scores_far_past_2_to_the_24(lq, lk, heads, D, lens, causal, sign):
         # lse = top + log l: log2(e), the product with it, ln 2 and the product with that, 2^-24 each
         assert (np.abs(gl[rows, h] - (top + np.log(l))) <=
                 2.0 ** -22 * np.abs(top) + err + 2.0 ** -22 * np.abs(np.log(l))).all()
+
+
+@pytest.mark.parametrize("name", ["256-row tiles", "128-row tiles", "few rows"])
+def test_sums_over_very_many_keys(name):
+    """Keys that are all alike: every weight is the same number, so that additions to a growing sum
+    all round the same way.  lse's bound does not grow with the number of keys: a score's error, a tile's
+    sum (2^-20 with the power of two and the logarithm), lse's own rounding.  out's sums are
+    rounded every 16 keys, its divisor's every tile: n / 16 2^-24 each at most."""
+    D, heads, seqs, lq, lk = {"256-row tiles": (8, 16, 1, 8192, 262144), "128-row tiles": (8, 16, 2, 4096, 131072),
+                              "few rows": (64, 1, 512, 1, 131072)}[name]
+    q, k = randn((seqs * lq, heads, D), 1), randn((1, heads, D), 2)
+    v = torch.full((1, heads, D), 1.25, dtype=torch.bfloat16, device="cuda")
+    say(f"sums over many keys, {name}")
+    if name == "few rows":  # all sequences share one cache
+        K, V = (t.expand(lk, heads, D).contiguous().unsqueeze(0).expand(seqs, lk, heads, D) for t in (k, v))
+        out, lse = lynx.attention(q.view(seqs, lq, heads, D), K, V, return_lse=True)
+    else:
+        K, V = (t.expand(seqs * lk, heads, D).contiguous() for t in (k, v))
+        cu = (offsets([lq] * seqs), offsets([lk] * seqs)) if seqs > 1 else (None, None)
+        out, lse = lynx.attention(q, K, V, *cu, return_lse=True)
+    qd, kd = q.double(), k.double()
+    s, spread = (qd * kd).sum(-1) * D ** -0.5, (qd * kd).abs().sum(-1) * D ** -0.5
+    want = s + np.log(lk)
+    tol = (D * 2.0 ** -23 + 2.0 ** -22) * spread + 2.0 ** -21 + 2.0 ** -20 + 2.0 ** -22 * want.abs()
+    err = (lse.double().reshape(want.shape) - want).abs()
+    say(f"lse off by {err.max().item():.2e}, {(err / tol).max().item():.3f} of its bound")
+    assert (err <= tol).all()
+    assert ((out.double() - 1.25).abs() <= 1.25 * (2.0 ** -8 + 2 * lk / 16 * 2.0 ** -24)).all()
