@@ -9,8 +9,8 @@
 // fit).  Angles cost fp64 arithmetic, so they are taken once a
 // token: the wave's lanes compute the cosines and sines of its pairs while the first rows are
 // under way, and each lane keeps those of its 8 channels for all heads.  The angle is taken in
-// turns, t = position * (frequency / 2 pi), and t - rint(t) is exact, so positions far from the
-// start lose nothing.
+// turns, t = position * (frequency / 2 pi), which is off by 2^-52 of itself at most (2^-23.6 of a
+// turn at position 2^31), and t - rint(t) is exact, before it is rounded to fp32 (2^-26).
 //
 // A pair's other channel is the lane's own (adjacent pairs) or lies R / 2 further: such rows cross
 // lanes through LDS, as bf16 words.  The norm's weights go into the factors:
@@ -298,13 +298,14 @@ lynx_status launch_qk_rotary(const lynx_rotary& d, hipStream_t stream) {
     for (int i = 0, p = 0; i < 4; ++i) {
         a.first[i] = i < d.axes ? p : a.pairs;
         if (i >= d.axes) continue;
-        // theta^(-2 j / n) as powers of theta^(-2 / n): 128 roundings of 2^-53 at most
+        // theta^(-2 j / n) as powers of theta^(-2 / n), in 64 bits of fraction, so that 128 products
+        // leave one rounding to 53 bits: in those they were off by 2^-21.9 of a turn at position 2^31
         const bool joint = d.ladder == LYNX_LADDER_JOINT;
-        const double step = std::pow(d.theta, -2.0 / (joint ? R : d.axis_dims[i]));
-        double f = 0.15915494309189535;  // 1 / 2 pi
+        const long double step = std::pow(static_cast<long double>(d.theta), -2.0L / (joint ? R : d.axis_dims[i]));
+        long double f = 0.159154943091895335768883763372514362L;  // 1 / 2 pi
         if (joint)
             for (int j = 0; j < p; ++j) f *= step;
-        for (int j = 0; j < d.axis_dims[i] / 2; ++j, f *= step) a.turns[p++] = f;
+        for (int j = 0; j < d.axis_dims[i] / 2; ++j, f *= step) a.turns[p++] = double(f);
     }
     const int halves = d.pairs == LYNX_PAIRS_ADJACENT ? 0 : a.pairs % 8 == 0 ? 1 : 2;
     // A token's groups go to several waves while there are fewer than three to a SIMD: what a wave

@@ -370,9 +370,9 @@ lynx_status lynx_block_norm(const lynx_norm* norm, lynx_stream_t stream);
  *                                                       share one row of frequencies.
  * Pair p is channels 2 p and 2 p + 1 (LYNX_PAIRS_ADJACENT), or p and p + R / 2
  * (LYNX_PAIRS_HALVES).  Channels from R on are normed but not turned.
- * Angles are taken in 64 bits and reduced to one turn before they are rounded, so that
- * they are as exact far from the start as near it; norm and turn are fp32, and there is
- * one rounding to bf16.
+ * Angles are taken in 64 bits, off by 2^-52 of themselves at most, and reduced to one turn
+ * before they are rounded to fp32 (2^-26 of a turn): an angle of 2^31 is within 2^-23 of a
+ * turn.  Norm and turn are fp32, and there is one rounding to bf16.
  *   - The turn is undone (the backward pass of a turn without a norm) by the same call
  *     with negated positions.
  *   - Strides are in elements, between tokens and between heads, multiples of 8, and

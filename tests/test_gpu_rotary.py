@@ -97,6 +97,50 @@ def test_far_positions(theta, f32):
     run(50, 2, 1, 128, (128,), theta=theta, far=2 ** 24, f32=f32, pairs="halves")
 
 
+@pytest.mark.parametrize("theta,axes", [(1.5, (256,)), (2.0, (128, 128)), (2.0, (128,)), (1e4, (128,))])
+@pytest.mark.parametrize("ladder", ["axis", "joint"])
+def test_angles_at_the_last_positions(theta, axes, ladder):
+    """Positions next to 2^31, and channels that nearly cancel, so that the result's own rounding hides
+    nothing.  An angle's frequency and the angle are rounded to 53 bits, 2^-52 of the angle together;
+    what is left of whole turns is rounded to fp32, half a turn at most: 2 pi 2^-26 < 2^-23.3; cosine and
+    sine are off by 2^-23 each, the products by 2^-24: (2^-52 angle + 2^-21.4) of the pair's size."""
+    LD = np.longdouble
+    T, R = 64, sum(axes)
+    g = np.random.default_rng(3)
+    pos = np.stack([2 ** 31 - 1 - g.integers(0, 1 << 20, T) for _ in axes], 1)
+    pos[::2] *= -1
+    angle, p = np.zeros((T, R // 2), dtype=LD), 0
+    for i, d in enumerate(axes):
+        for j in range(d // 2):
+            e = LD(j) / LD(d // 2) if ladder == "axis" else LD(p) / LD(R // 2)
+            angle[:, p] = pos[:, i].astype(LD) * LD(theta) ** -e
+            p += 1
+    c, s = np.cos(angle), np.sin(angle)
+
+    def bf16(x):
+        return torch.from_numpy(np.asarray(x, dtype=np.float64)).to(torch.bfloat16).double().numpy()
+
+    # x_m c = x_n s nearly: the larger of the two one of 128 numbers in [1, 2), the other rounded
+    lead = (1 + np.arange(128) / 128)[None, None].astype(LD)
+    big_m = np.abs(s) >= np.abs(c)
+    ratio = np.where(big_m, c / np.where(s == 0, 1, s), s / np.where(c == 0, 1, c))[..., None]
+    small = bf16(lead * ratio)
+    m = np.where(big_m[..., None], lead, small)
+    n = np.where(big_m[..., None], small, lead)
+    best = np.abs(m * c[..., None] - n * s[..., None]).argmin(-1)[..., None]
+    m, n = (np.take_along_axis(np.broadcast_to(t, m.shape), best, -1)[..., 0] for t in (m, n))
+    x = torch.zeros((T, 1, R), dtype=torch.bfloat16)
+    x[:, 0, 0::2], x[:, 0, 1::2] = torch.from_numpy(m.astype(np.float64)), torch.from_numpy(n.astype(np.float64))
+    say(f"last positions {theta} {axes} {ladder}")
+    got, _ = lynx.qk_rotary(x.cuda(), None, torch.from_numpy(pos.astype(np.int32)).cuda(), axes, theta,
+                            ladder=ladder)
+    want = (m * c - n * s).astype(np.float64)
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -52 * np.abs(angle) + 2.0 ** -21.4).astype(np.float64) * np.hypot(m, n)
+    err = np.abs(host_f64(got)[:, 0, 0::2] - want)
+    say(f"worst {np.max(err / tol):.3f} of its bound")
+    assert (err <= tol.astype(np.float64)).all()
+
+
 @pytest.mark.parametrize("pairs", ["adjacent", "halves"])
 def test_slices_of_a_projection_in_place(pairs):
     T, H, KV, D = 77, 6, 2, 72
