@@ -123,9 +123,13 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& A, int block, AttnItem
         r.lk = clampi(A.cu_k[s + 1], r.k0, A.tokens_k) - r.k0;
         return r;
     };
+    // (A grid has fewer workgroups than `most`.  Offsets that go back and forth make sequences of the
+    // same tokens, of which 65536 have more pieces in all than an int holds; these are cut off, and so
+    // are sums below, which then stay below 2^31.)
+    constexpr int most = (1 << 24) - 1;
     auto pieces = [&](const Range& r) {
         const AttnPlan<BM, BN> p(A, r.lq, r.lk);
-        return p.tiles * p.chunks;
+        return min(p.tiles * p.chunks, most);
     };
     const int xcd = block & 7, slot = block >> 3, share = 8 / A.classes;
     const int idx = slot * share + xcd / A.classes;
@@ -158,7 +162,7 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& A, int block, AttnItem
         per_head = __builtin_amdgcn_readlane(sum, min(A.batch, 64) - 1);
         if (A.batch > 64) {
             int n = 0;
-            for (int s = 64 + lane; s < A.batch; s += 64) n += pieces(range(s));
+            for (int s = 64 + lane; s < A.batch; s += 64) n = min(n + pieces(range(s)), most);
             per_head += __builtin_amdgcn_readlane(wave_scan(n, lane, 64), 63);
         }
     } else {

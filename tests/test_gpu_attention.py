@@ -395,6 +395,40 @@ def test_hidden_keys_of_few_rows_of_one_token(heads, D):
         assert torch.equal(out[..., rest], want[..., rest])
 
 
+@pytest.mark.parametrize("batch,tq,tk,heads,kv", [(3, 700, 900, 4, 2), (40, 40, 5000, 8, 2), (100, 9000, 4000, 2, 2),
+                                                  (9, 9, 20000, 2, 1)])
+@pytest.mark.parametrize("causal,P", [(False, 0), (True, 300)])
+def test_offsets_out_of_order_touch_nothing_else(batch, tq, tk, heads, kv, causal, P):
+    """Offsets that decrease or lie outside are held to the tensors: what is beside out and lse stays."""
+    q, k, v = randn((tq, heads, 64), 1), randn((tk, kv, 64), 2), randn((tk, kv, 64), 3)
+    kw = dict(causal=causal, prefix=(randn((P, kv, 64), 4), randn((P, kv, 64), 5)) if P else None)
+    rng = np.random.default_rng(batch)
+    for top in (tq + 5, 2 ** 31 - 1):
+        cq, ck = (torch.from_numpy(rng.integers(-top, top, batch + 1).astype(np.int32)).cuda() for _ in "qk")
+        out, lse = nan_bf16((tq + 512, heads, 64)), torch.full((tq + 512, heads), 7.0, device="cuda")
+        say(f"offsets in no order {batch} {tq} {tk} {top}")
+        lynx.attention(q, k, v, cq, ck, out=out[256:-256], lse=lse[256:-256], **kw)
+        torch.cuda.synchronize()
+        for t in (out[:256], out[-256:]):
+            assert (t.view(torch.int16) == 0x7FC0).all()
+        assert (lse[:256] == 7).all() and (lse[-256:] == 7).all()
+
+
+def test_offsets_that_go_back_and_forth():
+    """32768 sequences of all tokens each: 2^31 row tiles in all, of which the launch takes a part."""
+    batch, tq = 1 << 16, 1 << 21
+    q, k = randn((tq, 1, 8), 1), randn((8, 1, 8), 2)
+    cu = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = tq
+    out = nan_bf16((tq + 512, 1, 8))
+    say("offsets back and forth")
+    lynx.attention(q, k, k, cu, torch.zeros_like(cu), out=out[256:-256])
+    torch.cuda.synchronize()
+    for t in (out[:256], out[-256:]):
+        assert (t.view(torch.int16) == 0x7FC0).all()
+    assert (out[256:-256] == 0).all()  # no keys; the first sequence has all rows
+
+
 # ---- offsets past 32 bits ----------------------------------------------------------
 
 def test_a_cache_of_more_than_4_gib():
