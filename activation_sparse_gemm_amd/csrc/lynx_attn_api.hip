@@ -76,7 +76,7 @@ bool attn_sizes_ok(const lynx_attn& d) {
 lynx_status validate_attn(const lynx_attn& d, bool* noop) {
     *noop = false;
     if (!attn_sizes_ok(d)) return LYNX_ERR_SHAPE;
-    if (!(d.scale > 0.f) || !std::isfinite(d.scale)) return LYNX_ERR_SHAPE;
+    if (!(d.scale > 0.f) || !(d.scale < 0x1p127f)) return LYNX_ERR_SHAPE;  // (log2(e) times it is finite)
     if ((d.cu_q != nullptr) != (d.cu_k != nullptr)) return LYNX_ERR_NULL;
     if (!d.cu_q && (d.tokens_q % d.batch != 0 || d.tokens_k % d.batch != 0)) return LYNX_ERR_SHAPE;
     if (!strides_ok({d.q_stride, d.q_head_stride, d.k_stride, d.k_head_stride, d.v_stride,

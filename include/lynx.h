@@ -454,7 +454,7 @@ lynx_status lynx_qk_rotary(const lynx_rotary* rotary, lynx_stream_t stream);
  * Limits: head_dim a multiple of 8, 8..128; 1 <= kv_heads, heads a multiple of it, <= 1024;
  * 1 <= batch <= 2^16; tokens_q, tokens_k and prefix_tokens each 0..2^26 (tokens_q == 0
  * is a no-op), in the uniform form multiples of batch; tokens_q * heads < 2^30; batch *
- * kv_heads <= 2^21; scale > 0 and finite.  q, k, v, out and prefix pointers are 16-byte
+ * kv_heads <= 2^21; 0 < scale < 2^127.  q, k, v, out and prefix pointers are 16-byte
  * aligned, cu_* and lse 4-byte.  k and v may be NULL if tokens_k is 0.
  */
 typedef struct lynx_attn {

@@ -83,6 +83,14 @@ def test_attention_validation(kw, status):
     assert attn(**kw) == status
 
 
+def test_scales_that_pass_fp32_with_log2_e():
+    # above 2^128 / log2(e) = 2^127.47 every score that is 0 would become NaN
+    for scale in (2.0 ** 127, 3.4e38):
+        assert attn(scale=scale) == SHAPE
+    assert attn(scale=2.0 ** 127, tokens_q=0) == SHAPE
+    assert attn(scale=2.0 ** 127 * (1 - 2.0 ** -24), tokens_q=0) == OK and attn(scale=2.0 ** -149, tokens_q=0) == OK
+
+
 def test_null_descriptors():
     L = _abi.lib()
     assert L.lynx_qk_rotary(None, None) == NULL
