@@ -659,6 +659,8 @@ def qk_rotary(q, k, positions, axes, theta=10000.0, pairs="adjacent", ladder="ax
         if out is None:
             k_out = torch.empty(T, kv, D, dtype=torch.bfloat16, device=dev)
             ko, kot, koh = k_out.data_ptr(), kv * D, D
+        elif k_out is None:
+            raise ValueError("out: k needs a second output")
         else:
             ko, kot, koh = _heads(k_out, k.shape, dev, "k_out")
     elif k_out is not None:

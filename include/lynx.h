@@ -383,6 +383,8 @@ lynx_status lynx_block_norm(const lynx_norm* norm, lynx_stream_t stream);
  *   - A head whose row holds a NaN or an infinity, or whose squares pass fp32's range,
  *     becomes NaN throughout under a norm.  Without one, NaN and infinities reach their
  *     pair alone.  A position that is not finite makes its axis' pairs NaN.
+ *   - Squares below 2^-126 lose bits, and below 2^-149 all of them: with eps 0 a row whose
+ *     channels are all below 2^-63 is inexact, infinite or NaN under a norm.
  * Limits: head_dim a multiple of 8, 8..256; 1 to 4 axes, each of an even number >= 2
  * of channels, R <= head_dim; theta > 0 and finite; 0 <= tokens <= 2^24 (0 is a no-op);
  * 1 <= q_heads, 0 <= k_heads (0: k, k_out and k_weight are NULL), each <= 1024; tokens *

@@ -200,6 +200,13 @@ def test_values_that_are_not_finite(pairs, norm):
     assert torch.equal(got[~bad], want[~bad])
 
 
+def test_outputs_go_with_inputs():
+    x, pos = randn((3, 2, 64), 1), positions_of(3, 1, False, 2)
+    for k, out in ((x, (x, None)), (None, (x, x))):
+        with pytest.raises(ValueError, match="second output"):
+            lynx.qk_rotary(x, k, pos, (64,), out=out)
+
+
 def test_a_norm_of_zeros_and_of_small_rows():
     x = randn((4, 2, 64), 1)
     x[0] = 0
