@@ -43,7 +43,7 @@ lynx_status validate_rotary(const lynx_rotary& d, bool* noop) {
         R += d.axis_dims[i];
     }
     if (R > d.head_dim) return LYNX_ERR_SHAPE;
-    if (!(d.theta > 0.0) || !std::isfinite(d.theta)) return LYNX_ERR_SHAPE;
+    if (!(d.theta > 0.0) || !std::isnormal(d.theta)) return LYNX_ERR_SHAPE;  // (1 / theta is finite)
     if (d.pairs != LYNX_PAIRS_ADJACENT && d.pairs != LYNX_PAIRS_HALVES) return LYNX_ERR_SHAPE;
     if (d.ladder != LYNX_LADDER_AXIS && d.ladder != LYNX_LADDER_JOINT) return LYNX_ERR_SHAPE;
     if (d.norm != LYNX_NORM_NONE && d.norm != LYNX_NORM_RMS) return LYNX_ERR_SHAPE;

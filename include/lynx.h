@@ -386,7 +386,7 @@ lynx_status lynx_block_norm(const lynx_norm* norm, lynx_stream_t stream);
  *   - Squares below 2^-126 lose bits, and below 2^-149 all of them: with eps 0 a row whose
  *     channels are all below 2^-63 is inexact, infinite or NaN under a norm.
  * Limits: head_dim a multiple of 8, 8..256; 1 to 4 axes, each of an even number >= 2
- * of channels, R <= head_dim; theta > 0 and finite; 0 <= tokens <= 2^24 (0 is a no-op);
+ * of channels, R <= head_dim; theta normal and > 0; 0 <= tokens <= 2^24 (0 is a no-op);
  * 1 <= q_heads, 0 <= k_heads (0: k, k_out and k_weight are NULL), each <= 1024; tokens *
  * (q_heads + k_heads) < 2^31; eps >= 0.  Pointers are 16-byte aligned.
  */

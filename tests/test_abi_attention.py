@@ -83,6 +83,12 @@ def test_attention_validation(kw, status):
     assert attn(**kw) == status
 
 
+def test_bases_whose_frequencies_pass_64_bits():
+    # theta^(-2 j / n) reaches 1 / theta nearly; infinite ones made NaN of position 0
+    assert rotary(theta=5e-324) == SHAPE and rotary(theta=5e-324, tokens=0) == SHAPE
+    assert rotary(theta=2.0 ** -1022, tokens=0) == OK and rotary(theta=1e308, tokens=0) == OK
+
+
 def test_scales_that_pass_fp32_with_log2_e():
     # above 2^128 / log2(e) = 2^127.47 every score that is 0 would become NaN
     for scale in (2.0 ** 127, 3.4e38):
