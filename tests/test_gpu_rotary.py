@@ -284,3 +284,26 @@ def test_the_attention_half_of_a_block():
     say(f"block half: worst row {err.max():.2e}")
     assert err.max() <= 5e-2
     assert bo is not None
+
+
+def test_the_stages_before_the_turn():
+    """norm -> QKV, each against 64 bits of its own input (the block's half above starts at their result).
+
+    h: rounded once, 2^-8; before it mean, variance, their factor and the shift in fp32: sums of C terms
+    in trees and chains of less than 2^6, so 2^-17 of the magnitudes that are added.  qkv: rounded once, and
+    C products summed in fp32, C 2^-24 of their magnitudes."""
+    n, C = 257, 256
+    x, W = randn((n, C), 1), randn((3 * C, C), 2, C ** -0.5)
+    scale, shift = randn((1, C), 4, 0.3), randn((1, C), 5, 0.3)
+    say("norm and projection before the turn")
+    h = lynx.norm_modulate(x, "layer", scale=scale, shift=shift)
+    qkv = lynx.linear_dense(h, W)
+    X = host_f64(x)
+    t = X - X.mean(1, keepdims=True)
+    f = (1 + host_f64(scale)) / np.sqrt((t * t).mean(1, keepdims=True) + 1e-6)
+    want = t * f + host_f64(shift)
+    mag = (np.abs(X) + np.abs(X).mean(1, keepdims=True)) * np.abs(f) + np.abs(host_f64(shift))
+    assert (np.abs(host_f64(h) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -17 * mag).all()
+    H, Wn = host_f64(h), host_f64(W)
+    want = H @ Wn.T
+    assert (np.abs(host_f64(qkv) - want) <= 2.0 ** -8 * np.abs(want) + C * 2.0 ** -24 * (np.abs(H) @ np.abs(Wn).T)).all()
