@@ -1,7 +1,7 @@
 // Attention of few query rows to a key head, as a kernel of its own; and side by side with tiles
 // of 128 rows, for a prefix that the batch shares: all sequences' rows together on the prefix, each
 // sequence's rows on its own keys.  48 tokens on a prefix of 8192 and up to 512 keys of their own,
-// 32/8 x 128: 26 us, and 5 for the join (side by side saved 4 of 43 us, cutting the prefix for it 8).
+// 32/8 x 128: 27 us, and 5 for the join (side by side saved 4 of 43 us, cutting the prefix for it 8).
 #include "lynx_attn_few.h"
 #include "lynx_attn_tile.h"
 

@@ -4,8 +4,8 @@
 // rows of Q while it works on the present ones, and multiplies the first tile's scores of the next
 // rows together with the last tile's values of the present ones.
 //
-// 2 x 4096 rows on 300 keys, 16 x 72: 26 us, of which 5 until the keys are there and 14 for two row tiles to a
-// wave (tiles of 128 rows, that each fetch the keys: 34); 20000 on 300, 28/4 x 128: 120 us, 715 TFLOP/s
+// 2 x 4096 rows on 300 keys, 16 x 72: 25 us, of which 5 until the keys are there and 14 for two row tiles to a
+// wave (tiles of 128 rows, that each fetch the keys: 34); 20000 on 300, 28/4 x 128: 117 us, 737 TFLOP/s
 // (179).  Two waves of a SIMD take 3500 cycles for a step each (96 channels), the products of it 1584 and
 // the weights 1800: nothing makes the waves alternate, and priorities made no difference.
 #include "lynx_attn_wave.h"

@@ -13,8 +13,8 @@
 // when the barrier opens, a slot before group 0 multiplies them, so that each group reads its
 // first operands ahead, at the end of its weighing.
 //
-// The board's power bounds it: 16384 x 16384 x 8 heads x 128 950 us, 1160 TFLOP/s, the matrix cores busy
-// 61% of the cycles at 1.7 GHz (tiles of 128 rows: 1058 us).  Measured and not kept: 64 rows to a
+// The weighing bounds a slot, and the board's power the clock: 16384 x 16384 x 8 heads x 128 942 us, 1167
+// TFLOP/s, the matrix cores busy 61% of the cycles at 1.84 GHz of 2.4 (tiles of 128 rows: 1058 us).  Measured and not kept: 64 rows to a
 // wave, which halves the reads from LDS, but does not fit 256 registers (accumulators in the other
 // half are copied for every factor); priorities of waves (no difference); loads inside the
 // multiplying (4608 x 4608 x 24 heads 290 us instead of 257).  The causal form sets registers aside
