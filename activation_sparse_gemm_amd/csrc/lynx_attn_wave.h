@@ -244,10 +244,11 @@ struct AttnWave {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[d][e] *= f;
     }
-    // Lanes whose row's |m| may be 2^24 or more after raise(top).  (Where m is below -2^24 and top is not,
-    // m is raised.)
-    __device__ __forceinline__ uint64_t far(float top) const { return __ballot(fmaxf(fabsf(top), m) >= 16777216.f); }
-    __device__ __forceinline__ bool near() const { return fabsf(m) < 16777216.f; }
+    // Lanes whose row's |m| is 2^29 or more after raise(top).  (Where m is -2^29 or below and top is not,
+    // m is raised: m + 8 is m there.  From 2^24 on m + 8 may still be more, and top between the two.)
+    static constexpr float kFar = 536870912.f;
+    __device__ __forceinline__ uint64_t far(float top) const { return __ballot(fmaxf(fabsf(top), m) >= kFar); }
+    __device__ __forceinline__ bool near() const { return fabsf(m) < kFar; }
     __device__ __forceinline__ static float apart(float v, float c, float from) {
 #pragma clang fp contract(off)
         const float t = v * c;
@@ -414,8 +415,9 @@ struct AttnTile : AttnWave<DP, LSE> {
     }
     // Raises m to a tile's scores, before their weights.  A multiply-add takes c s as it is, and m is
     // fp32: from 2^24 on, c s - m of a row's largest score is what m has lost, up to half its last
-    // place, which passes 2^7 from 2^31 on (weights of infinity, or of 0 alone).  In such rows c s is
-    // rounded as m was, and the scores become those that are as far from 0 as c s was from m.
+    // place.  That is 2^4 below 2^29, which changes all weights of a row alike, but past 2^7 from 2^31
+    // on (weights of infinity, or of 0 alone).  In rows past 2^29 c s is rounded as m was, and the
+    // scores become those that are as far from 0 as c s was from m.
     __device__ __forceinline__ void relate(float top, float c) {
         // (early, since a branch waits for its condition: 16384 x 16384 x 8 heads 980 us without, 993 so,
         // 998 with the condition after m is raised)

@@ -432,12 +432,13 @@ lynx_status lynx_qk_rotary(const lynx_rotary* rotary, lynx_stream_t stream);
  * already holds their own keys).  With a prefix (prefix_tokens > 0), every query of every
  * sequence also sees all prefix keys, which come before the sequence's own; causal
  * concerns own keys alone.  A query that sees no key gets out = 0 and lse = -infinity.
- *   - Scores and sums are fp32.  p_j, taken relative to a power of two no further than 2^9
- *     below the row's largest, is rounded to bf16, for its product with v_j and for out's
- *     divisor alike (lse sums the p_j before that); out has one more rounding.  out's sums
- *     round once for every 16 keys (n / 16 2^-24 relative at most), lse's sum keeps what its
- *     additions lose.  A row's result does not depend on what other rows hold, and is the same
- *     in every call of the same sizes, offsets and strides.
+ *   - Scores, times scale too, and sums are fp32.  p_j, taken relative to a power of two no
+ *     further than 2^9 below the row's largest (2^25 for scores past 2^23), is rounded to
+ *     bf16, for its product with v_j and for out's divisor alike (lse sums the p_j before
+ *     that); out has one more rounding.  out's sums round once for every 16 keys (n / 16 2^-24
+ *     relative at most), lse's sum keeps what its additions lose.  A row's result does not
+ *     depend on what other rows hold, and is the same in every call of the same sizes, offsets
+ *     and strides.
  *   - Keys that a query does not see have no influence on it, whatever they hold; with
  *     NaN or infinities among the keys and values that it sees, its row is as the
  *     formula gives it (an infinite or NaN value whose p_j is 0 makes NaN), and so with a

@@ -67,6 +67,53 @@ def test_scores_far_past_2_to_the_24(lq, lk, heads, D, lens, causal, sign):
                 2.0 ** -22 * np.abs(top) + err + 2.0 ** -22 * np.abs(np.log(l))).all()
 
 
+@pytest.mark.parametrize("lq,lk,heads", [(130, 300, 2), (3, 4000, 2), (4100, 300, 16), (2048, 2048, 16)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("power", [24, 28, 29, 30])
+def test_scores_on_both_sides_of_a_power_of_two(lq, lk, heads, sign, power):
+    """Scores, exact in fp32, that are next to sign * 2^power once they are times log2(e), the first 200 keys'
+    a little further down than the others': e^-d of each other, d whole numbers times a score's last place."""
+    D = 64
+    big = int(2.0 ** power / 1.4426950408889634)
+    last = max(1, 2 ** (power - 24))                # a score's last place
+    big = big // last * last
+    step = last if power < 29 else 4 * last
+    pieces, left = [], big
+    for _ in range(3):                              # bf16 numbers that add up to it
+        unit = 2 ** max(0, left.bit_length() - 8)
+        pieces.append(left // unit * unit)
+        left -= pieces[-1]
+    assert left == 0 and sum(pieces) == big
+    rng = np.random.default_rng(power)
+    d = rng.integers(-4, 5, lk)
+    d[:200] = rng.integers(1, 5, 200)               # first those of small weight
+    d[-3:] = -3
+    q = torch.zeros((lq, heads, D), dtype=torch.bfloat16, device="cuda")
+    q[..., :4] = 1
+    k = torch.zeros((lk, heads, D), dtype=torch.bfloat16, device="cuda")
+    for i, p in enumerate(pieces):
+        k[..., i] = sign * p
+    k[..., 3] = torch.from_numpy(-d * step).to(torch.bfloat16).cuda()[:, None]
+    v = randn((lk, heads, D), 3)
+    say(f"around 2^{power} {lq} {lk} {sign}")
+    out, lse = lynx.attention(q, k, v, scale=1.0, return_lse=True)
+    p = np.exp(-(d - d.min()).astype(np.float64) * step)
+    vn = host_f64(v)
+    l = p.sum()
+    want = np.einsum("j,jhd->hd", p, vn) / l
+    dev = np.sqrt(np.maximum(np.einsum("j,jhd->hd", p, vn ** 2) / l - want ** 2, 0))
+    # the factor log2(e) is off by 2^-24 of a difference of 8 steps at most; p and out are rounded.  (Past 2^29
+    # the product is off by half its last place, 32 or 64 at most where a step is 128 or 256: the weights of keys
+    # that are a step down are 0 either way, and alike keys have alike weights.)
+    err = 8 * step * 2.0 ** -23 + 2.0 ** -20 + lk * 2.0 ** -23
+    tol = (2.0 ** -8 + 2 * err) * (dev + np.abs(want)) + 1e-30
+    got = host_f64(out)
+    assert (np.abs(got - want[None]) <= tol[None]).all()
+    top = sign * float(big) - d.min() * step
+    gl = lse.cpu().numpy().astype(np.float64)
+    assert (np.abs(gl - (top + np.log(l))) <= 2.0 ** -22 * abs(top) + 1e-3).all()
+
+
 @pytest.mark.parametrize("name", ["256-row tiles", "128-row tiles", "few rows"])
 def test_sums_over_very_many_keys(name):
     """Keys that are all alike: every weight is the same number, so that additions to a growing sum
